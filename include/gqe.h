@@ -381,6 +381,192 @@ int64_t gqe_workspace_bytes(int dim, int N, int G, int k, int d_h, gqe_dtype dty
  * (-1 for a null handle). */
 int gqe_kernel_launches(gqe_handle h);
 
+/* =======================================================================================
+ * Operators on the layer's streams, without a handle: the norm and rotation of queries and
+ * keys, and attention whose scores are capped, biased or masked. They allocate nothing and do
+ * not synchronise; scratch is the caller's. The layer runs the same kernels when they are set
+ * on a handle (gqe_set_qk_transform, gqe_set_scores).
+ * ======================================================================================= */
+
+/* gqe_heads — rows of d_h values in the caller's device memory: head h's row of token t starts
+ * at data + h * head_stride + t * token_stride (in elements). Rows are dense, data is 16-byte
+ * aligned and the strides are multiples of 16 bytes; token_stride >= d_h where there is more
+ * than one token, head_stride >= d_h where there is more than one head. [heads, tokens, d_h] has
+ * strides (tokens * d_h, d_h); [tokens, heads, d_h] has (d_h, heads * d_h). */
+typedef struct {
+    void* data;
+    int heads;
+    int64_t head_stride;
+    int64_t token_stride;
+} gqe_heads;
+
+/* gqe_qk_transform — RMS norm over the head dimension and rotation by position.
+ *   norm       1: h = w * x / sqrt(mean(x^2) + eps); 0: h = x.
+ *   q_weight,  [d_h] float32, device: w of the query and the key heads; NULL: ones.
+ *   k_weight
+ *   rot_dim    the first rot_dim values of a head are rotated in pairs: a multiple of 16, 0
+ *              (none) to d_h. Pair i turns by position * inv_freq[i].
+ *   interleaved  0: pair i is (i, i + rot_dim/2); 1: (2i, 2i + 1).
+ *   inv_freq   [rot_dim/2] float64, device: radians per position. Angles are formed in 64
+ *              bits, so far positions keep their place in the turn.
+ * d_h as gqe_create; dtype GQE_BF16 or GQE_F32 (of every gqe_heads of the call). */
+typedef struct {
+    int d_h;
+    int dtype;
+    int norm;
+    float eps;
+    const float* q_weight;
+    const float* k_weight;
+    int rot_dim;
+    int interleaved;
+    const double* inv_freq;
+} gqe_qk_transform;
+
+/*
+ * gqe_qk_norm_rope — norm and rotation of M tokens' query and key heads in one pass.
+ *   q, k        inputs; either may have 0 heads. At most 512 heads each.
+ *   positions   [M] int32, device; NULL: token t has position t % T (T >= 1).
+ *   q_out, k_out  outputs, as many heads as the inputs; may be the inputs themselves.
+ * M = 0 does nothing. Arithmetic in float32, one rounding to the dtype.
+ */
+gqe_status gqe_qk_norm_rope(const gqe_qk_transform* tr, int M, const gqe_heads* q,
+                            const gqe_heads* k, const int32_t* positions, int T,
+                            const gqe_heads* q_out, const gqe_heads* k_out, void* stream);
+
+/* gqe_qk_norm_rope_workspace_bytes — scratch of a backward call that asks for weight
+ * gradients (-1 for an unsupported d_h). */
+int64_t gqe_qk_norm_rope_workspace_bytes(int d_h);
+
+/*
+ * gqe_qk_norm_rope_backward — gradients of gqe_qk_norm_rope.
+ *   q, k           the forward's inputs (not its outputs).
+ *   dq_out, dk_out upstream gradients of its outputs.
+ *   dq, dk         written: gradients of q and k (may be dq_out and dk_out themselves).
+ *   dq_weight,     [d_h] float32, device, written (not accumulated into): gradients of the
+ *   dk_weight      weights, zeros without a norm; NULL: not wanted.
+ *   workspace      gqe_qk_norm_rope_workspace_bytes bytes on the device, 16-byte aligned, where
+ *                  a weight gradient is wanted (NULL otherwise). Used until the call's kernels
+ *                  end: calls that may run at the same time need one each.
+ * The result is the same from run to run (no atomics).
+ */
+gqe_status gqe_qk_norm_rope_backward(const gqe_qk_transform* tr, int M, const gqe_heads* q,
+                                     const gqe_heads* k, const int32_t* positions, int T,
+                                     const gqe_heads* dq_out, const gqe_heads* dk_out,
+                                     const gqe_heads* dq, const gqe_heads* dk, float* dq_weight,
+                                     float* dk_weight, void* workspace, size_t bytes,
+                                     void* stream);
+
+/*
+ * gqe_qk_norm_rope_append — the serving form: one new token per sequence. Rotates and norms
+ * the B new tokens' queries into q_out and their keys into row lengths[b] of the key cache,
+ * and copies their values into the same row of the value cache, in one launch.
+ *   q, k, v      the new tokens (token b belongs to sequence b); k and v with equal heads.
+ *   lengths      [B] int32, device: positions of the new tokens, which are also their cache
+ *                rows, 0 <= lengths[b] < L_max. -1 marks an idle slot: nothing of sequence b
+ *                is written. Another value writes nothing either and is reported by
+ *                gqe_check_op_status (GQE_ERR_INVALID_ARG).
+ *   k_cache,     [G, B, L_max, d_h]: token_stride is the stride between sequences, rows of a
+ *   v_cache      sequence are dense (token_stride >= L_max * d_h for more than one sequence).
+ * No other row is written.
+ */
+gqe_status gqe_qk_norm_rope_append(const gqe_qk_transform* tr, int B, const gqe_heads* q,
+                                   const gqe_heads* k, const gqe_heads* v,
+                                   const int32_t* lengths, int L_max, const gqe_heads* q_out,
+                                   const gqe_heads* k_cache, const gqe_heads* v_cache,
+                                   void* stream);
+
+/* gqe_scores — attention of S query streams over G KV heads whose scores may be capped, biased
+ * and masked. Query t of a sequence sees the keys u with key_begin[t] <= u < key_end[t], and
+ * u <= t when causal; its scores are
+ *     z = scale <q_t, k_u>;  z = softcap tanh(z / softcap);  z -= slopes[s] |t - u|
+ * and its weights the softmax of z over those keys. A row that sees no key gives zeros and has
+ * no gradient. What is masked may hold anything: infinities and NaN in keys and values reach
+ * only the rows that see them (as NaN).
+ *   B, T        sequences and tokens of each; tokens are sequence-major (b T + t).
+ *   G, k, S     stream s < G k reads KV head s / k; S = G k, or G k + 1 with a last stream
+ *               that reads KV head 0 (the layer's shared head).
+ *   scale       > 0, or 0 for 1 / sqrt(d_h).
+ *   softcap     > 0, or 0 for none.
+ *   slopes      [S] float32, device, or NULL for no bias.
+ *   key_begin,  [B T] int32, device, positions within the sequence, or NULL for 0 and T; values
+ *   key_end     outside [0, T] are cut to it. Documents packed in a sequence: the first key
+ *               of the query's document (and its end, if not causal). A bidirectional prefix
+ *               of p tokens: causal 0, end max(t + 1, p). A sliding window of w: begin
+ *               t + 1 - w. Padding: end 0 for the rows behind the sequence, its length
+ *               elsewhere.
+ * Tensors are bf16 (gqe_heads of S or G heads); d_h as gqe_create; B T <= 2^27. */
+typedef struct {
+    int B;
+    int T;
+    int G;
+    int k;
+    int S;
+    int d_h;
+    int causal;
+    float scale;
+    float softcap;
+    const float* slopes;
+    const int32_t* key_begin;
+    const int32_t* key_end;
+} gqe_scores;
+
+/*
+ * gqe_attention_forward — out[s, b T + t] = sum of the weights times the values.
+ *   lse   [S, B T] float32, device, 4-byte aligned, or NULL: written for the backward pass, the
+ *         log2 of the row's sum of 2^(z log2 e) (-inf for a row without keys), as accurate as
+ *         the bf16 weights need (2^-9 relative in the sum).
+ * out must not overlap the inputs. B = 0 or T = 0 does nothing. One kernel launch; the result
+ * is the same from run to run. A wait inside the kernel that gives up is reported by
+ * gqe_check_op_status.
+ */
+gqe_status gqe_attention_forward(const gqe_scores* a, const gqe_heads* q, const gqe_heads* k,
+                                 const gqe_heads* v, const gqe_heads* out, float* lse,
+                                 void* stream);
+
+/* gqe_attention_workspace_bytes — scratch of gqe_attention_backward (-1: invalid sizes). */
+int64_t gqe_attention_workspace_bytes(const gqe_scores* a);
+
+/*
+ * gqe_attention_backward — gradients of gqe_attention_forward, given its inputs, out and lse, and
+ * the upstream gradient dout: dq [S heads], dk and dv [G heads, summed over their streams] are
+ * written (not accumulated into). `workspace`: gqe_attention_workspace_bytes bytes on the
+ * device, 16-byte aligned, used until the call's kernels end. No atomics: the result is the
+ * same from run to run. The slopes and intervals get no gradient.
+ */
+gqe_status gqe_attention_backward(const gqe_scores* a, const gqe_heads* q, const gqe_heads* k,
+                                  const gqe_heads* v, const gqe_heads* out, const float* lse,
+                                  const gqe_heads* dout, const gqe_heads* dq,
+                                  const gqe_heads* dk, const gqe_heads* dv, void* workspace,
+                                  size_t bytes, void* stream);
+
+/* gqe_attention_decode_workspace_bytes — scratch of gqe_attention_decode for caches of L_max
+ * rows on the current device (-1: invalid sizes). */
+int64_t gqe_attention_decode_workspace_bytes(const gqe_scores* a, int L_max);
+
+/*
+ * gqe_attention_decode — the single-token form: each of a->B sequences has one query per stream
+ * at position lengths[b] and attends over rows key_begin[b] (0 if NULL) .. lengths[b] of its
+ * caches, which hold its own key and value already (gqe_qk_norm_rope_append). a->T, causal and
+ * key_end are not used; key_begin is [B] here; k <= 8.
+ *   q, out    [S, B, d_h]; k_cache, v_cache as gqe_qk_norm_rope_append, [G, B, L_max, d_h].
+ *   lengths   [B] int32, device, -1 <= lengths[b] < L_max. -1: no key, out is zeros. Another
+ *             value leaves the sequence's out as it was and is reported by
+ *             gqe_check_op_status (GQE_ERR_INVALID_ARG).
+ *   workspace gqe_attention_decode_workspace_bytes bytes, 16-byte aligned (may be NULL for 0).
+ */
+gqe_status gqe_attention_decode(const gqe_scores* a, const gqe_heads* q,
+                                const gqe_heads* k_cache, const gqe_heads* v_cache, int L_max,
+                                const int32_t* lengths, const gqe_heads* out, void* workspace,
+                                size_t bytes, void* stream);
+
+/*
+ * gqe_check_op_status — synchronise `stream`, then read and clear the current device's status
+ * word of the operators above: GQE_OK, GQE_ERR_TIMEOUT (a wait gave up: outputs since the last
+ * check are invalid) or GQE_ERR_INVALID_ARG (a position outside its cache). Not while a stream
+ * is being captured.
+ */
+gqe_status gqe_check_op_status(void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,1016 @@
+// Tensor-core (tcgen05) backward pass of the attention with capped, biased and masked scores
+// (the forward's mathematics is in attn_scores.cuh). With p = softmax(z) over a row's keys,
+// D = <dout, out>, dP = dout v^T:
+//   dz = p (dP - D),  times 1 - tanh^2 where the scores are capped,
+//   dq = scale dz k,  dk = scale sum over the head's streams of dz^T q,
+//   dv = sum over the head's streams of p^T dout.
+//
+// Three kernels, none with atomics (every output row is written by one CTA, so results are
+// the same from run to run):
+//   attn_scores_d_kernel     D of every row, and the union of the intervals of every 128 rows;
+//   attn_scores_dq_kernel    CTA = (sequence, stream, 128-query tile); per 64-key step S = Q K^T
+//                            and dP into TMEM, dz in bf16 back to TMEM, dQ += dz K.
+//   attn_scores_dkdv_kernel  CTA = (sequence, KV head, 128-key tile); per job (a stream of the
+//                            head, a tile of queries) S^T and dP^T, then dV += p^T dout and
+//                            dK += dz^T Q, accumulated in TMEM over all the head's streams.
+// Scores and weights are formed again from the saved log-sum-exp rather than read: T^2 values
+// per stream would be the largest traffic by far. p and dz are rounded to bf16, the type of
+// the products' operands; D, the sums and the accumulators stay in 32 bits. Steps and jobs
+// outside the rows' intervals are never loaded; those that some row sees only in part are
+// masked, and their key (or query and dout) tiles are cleaned of infinities and NaN, which a
+// weight of zero would not keep out of a product.
+#include <cudaTypedefs.h>
+#include <limits.h>
+#include <string.h>
+
+#include <type_traits>
+
+#include "attn_scores.cuh"
+
+namespace gqe {
+namespace {
+
+using namespace tc;
+
+constexpr int THREADS = 256;
+constexpr int TQ = 128, TK = 128;
+constexpr int kSmallRegs = 48, kLargeRegs = 208;  // as the forward's register split
+static_assert(kSmallRegs * 128 + kLargeRegs * 128 == THREADS * (65536 / (2 * THREADS)),
+              "register split must equal the launch allocation");
+
+template <int DH>
+struct BCfg {
+  static constexpr int CW = (DH % 64 == 0) ? 64 : 16;  // 128- or 32-byte swizzle
+  static constexpr uint32_t LAYOUT = CW == 64 ? kSwizzle128B : kSwizzle32B;
+  static constexpr int ROW_BYTES = CW * 2;
+  static constexpr int TILE_BYTES = 128 * DH * 2;
+  static constexpr int CTAS = DH <= 64 ? 2 : 1;
+  static constexpr int TMEM_COLS = CTAS == 2 ? 256 : 512;
+  static constexpr int STAGES = 3;
+};
+
+struct Params {
+  CUtensorMap tm_q, tm_do, tm_k, tm_v;  // dQ: 128-row q, dout; 64-row k, v. dK / dV: job-row
+                                        // q, dout; 128-row k, v
+  SpanArgs span;
+  const float* lse;
+  const float* dsum;
+  const float* slopes;
+  const int2* blocks;
+  __nv_bfloat16* dq;
+  __nv_bfloat16* dk;
+  __nv_bfloat16* dv;
+  int64_t dq_hs, dq_ts, dk_hs, dk_ts, dv_hs, dv_ts;
+  const int32_t* sel;
+  __nv_bfloat16* dq_shared;
+  int64_t sel_stride;
+  int sel_off, experts;
+  int T, B, S, Sr, k, G, nq;
+  float scale, scale_log2, cap_in, cap_log2;
+  int32_t* status;
+  int64_t spin;
+};
+
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const Params& P) {
+  const bool ok = !__any_sync(0xffffffffu, !mbar_wait(bar, parity, P.spin));
+  if (!ok && (threadIdx.x & 31) == 0) atomicExch(P.status, kStatusTimeout);
+  return ok;
+}
+__device__ __forceinline__ bool lane_wait(uint64_t* bar, uint32_t parity, const Params& P) {
+  if (mbar_wait(bar, parity, P.spin)) return true;
+  atomicExch(P.status, kStatusTimeout);
+  return false;
+}
+
+template <int DH, int ROWS>
+__device__ __forceinline__ uint32_t kmajor_off(int kk) {
+  using C = BCfg<DH>;
+  return (((kk * 16) / C::CW) * ROWS * C::ROW_BYTES + ((kk * 16) % C::CW) * 2) >> 4;
+}
+
+// TMEM -> registers, N consecutive 32-bit columns per lane (N = 32, 48 or 64).
+template <int N>
+__device__ __forceinline__ void tmem_ldN_wait(uint32_t taddr, uint32_t (&r)[N]) {
+  static_assert(N == 32 || N == 48 || N == 64, "TMEM row widths of a job");
+  if constexpr (N == 64) {
+    tmem_ld64_wait(taddr, r);
+  } else {
+    uint32_t a[32];
+    tmem_ld32(taddr, a);
+    uint32_t b[16];
+    if constexpr (N == 48) tmem_ld16(taddr + 32, b);
+    // the wait names the registers it completes, so no use of them can move above it
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(a[0]), "+r"(a[1]), "+r"(a[2]), "+r"(a[3]), "+r"(a[4]), "+r"(a[5]),
+                   "+r"(a[6]), "+r"(a[7]), "+r"(a[8]), "+r"(a[9]), "+r"(a[10]), "+r"(a[11]),
+                   "+r"(a[12]), "+r"(a[13]), "+r"(a[14]), "+r"(a[15])
+                 :
+                 : "memory");
+    asm volatile("" : "+r"(a[16]), "+r"(a[17]), "+r"(a[18]), "+r"(a[19]), "+r"(a[20]),
+                      "+r"(a[21]), "+r"(a[22]), "+r"(a[23]), "+r"(a[24]), "+r"(a[25]),
+                      "+r"(a[26]), "+r"(a[27]), "+r"(a[28]), "+r"(a[29]), "+r"(a[30]),
+                      "+r"(a[31]));
+#pragma unroll
+    for (int i = 0; i < 32; ++i) r[i] = a[i];
+    if constexpr (N == 48) {
+      asm volatile("" : "+r"(b[0]), "+r"(b[1]), "+r"(b[2]), "+r"(b[3]), "+r"(b[4]), "+r"(b[5]),
+                        "+r"(b[6]), "+r"(b[7]), "+r"(b[8]), "+r"(b[9]), "+r"(b[10]),
+                        "+r"(b[11]), "+r"(b[12]), "+r"(b[13]), "+r"(b[14]), "+r"(b[15]));
+#pragma unroll
+      for (int i = 0; i < 16; ++i) r[32 + i] = b[i];
+    }
+  }
+}
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+      : "memory");
+}
+
+// A score of the products in log2 units (capped, biased) and the cap's derivative factor.
+template <bool CAP, bool BIAS>
+__device__ __forceinline__ float score(const Params& P, float s, float slope2, float dist,
+                                       float& dcap) {
+  float z;
+  if constexpr (CAP) {
+    const float th = tanh_from_2log2(s * P.cap_in);
+    dcap = fmaf(-th, th, 1.f);
+    z = th * P.cap_log2;
+  } else {
+    dcap = 1.f;
+    z = s * P.scale_log2;
+  }
+  if constexpr (BIAS) z = fmaf(-slope2, fabsf(dist), z);
+  return z;
+}
+
+// Runs f with the compile-time flags of the score's form (the same for the whole grid).
+template <typename F>
+__device__ __forceinline__ void by_form(bool cap, bool bias, F&& f) {
+  using Yes = std::integral_constant<bool, true>;
+  using No = std::integral_constant<bool, false>;
+  if (cap) {
+    if (bias) f(Yes{}, Yes{});
+    else f(Yes{}, No{});
+  } else {
+    if (bias) f(No{}, Yes{});
+    else f(No{}, No{});
+  }
+}
+
+// Writes a TMEM accumulator row (DH columns, scaled) as bf16.
+template <int DH>
+__device__ __forceinline__ void store_row(uint32_t taddr, __nv_bfloat16* dst, float sc, bool write,
+                                          bool zero) {
+#pragma unroll
+  for (int c0 = 0; c0 < DH; c0 += 16) {
+    uint32_t r[16];
+    tmem_ld16_wait(taddr + c0, r);
+    if (write) {
+      uint32_t w[8];
+#pragma unroll
+      for (int x = 0; x < 8; ++x)
+        w[x] = zero ? 0u
+                    : pack_bf16x2(__uint_as_float(r[2 * x]) * sc, __uint_as_float(r[2 * x + 1]) * sc);
+      *reinterpret_cast<uint4*>(dst + c0) = make_uint4(w[0], w[1], w[2], w[3]);
+      *reinterpret_cast<uint4*>(dst + c0 + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+    }
+  }
+}
+template <int DH>
+__device__ __forceinline__ void zero_row(__nv_bfloat16* dst) {
+#pragma unroll
+  for (int c0 = 0; c0 < DH; c0 += 8) *reinterpret_cast<uint4*>(dst + c0) = make_uint4(0, 0, 0, 0);
+}
+
+// ---------------------------------------------------------------------------------------
+// D = <dout, out> of every row (blockIdx.y: stream), and of every 128 rows the union of their
+// intervals (stream 0's blocks). Lanes of a row hold 8 values each.
+// ---------------------------------------------------------------------------------------
+constexpr int D_ROWS = 128;
+template <int DH>
+__global__ void __launch_bounds__(THREADS)
+attn_scores_d_kernel(QkTensor dout, QkTensor out, float* dsum, int2* blocks, SpanArgs span, int B,
+                     int nq, int given) {
+  constexpr int LANES = DH / 8;
+  constexpr int LPR = LANES <= 2 ? 2 : LANES <= 4 ? 4 : LANES <= 8 ? 8 : 16;
+  constexpr int RPB = THREADS / LPR;
+  pdl_wait();
+  pdl_allow_next();
+  const int b = blockIdx.x / nq, qt = blockIdx.x % nq, s = blockIdx.y;
+  const int l = threadIdx.x % LPR;
+  if (!given) {
+#pragma unroll
+    for (int r0 = 0; r0 < D_ROWS; r0 += RPB) {
+      const int t = qt * D_ROWS + r0 + threadIdx.x / LPR;
+      float d = 0.f;
+      if (t < span.T && l < LANES) {
+        const int64_t tok = (int64_t)b * span.T + t;
+        const uint4 x = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(dout.data) +
+                                                        s * dout.head_stride +
+                                                        tok * dout.token_stride + 8 * l);
+        const uint4 y = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(out.data) +
+                                                        s * out.head_stride +
+                                                        tok * out.token_stride + 8 * l);
+        const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          d = fmaf(__uint_as_float(xs[i] << 16), __uint_as_float(ys[i] << 16), d);
+          d = fmaf(__uint_as_float(xs[i] & 0xffff0000u), __uint_as_float(ys[i] & 0xffff0000u), d);
+        }
+      }
+#pragma unroll
+      for (int o = LPR / 2; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+      if (t < span.T && l == 0) dsum[(int64_t)s * B * span.T + (int64_t)b * span.T + t] = d;
+    }
+  }
+  if (!blocks || s != 0) return;
+  __shared__ int2 part[D_ROWS / 32];
+  if (threadIdx.x < D_ROWS) {
+    int b0, e0;
+    span_of(span, b, qt * D_ROWS + threadIdx.x, b0, e0);
+    const bool live = b0 < e0;
+    const int lo = __reduce_min_sync(0xffffffffu, live ? b0 : INT_MAX);
+    const int hi = __reduce_max_sync(0xffffffffu, live ? e0 : 0);
+    if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = make_int2(lo, hi);
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    int2 v = part[0];
+#pragma unroll
+    for (int i = 1; i < D_ROWS / 32; ++i) v = make_int2(min(v.x, part[i].x), max(v.y, part[i].y));
+    blocks[(int64_t)b * nq + qt] = v;
+  }
+}
+
+// ---------------------------------------------------------------------------------------
+// dQ
+// ---------------------------------------------------------------------------------------
+template <int DH>
+struct QCfg {
+  using C = BCfg<DH>;
+  static constexpr int TKD = 64;                 // keys per step
+  static constexpr int KT_BYTES = TKD * DH * 2;  // one 64-row K or V tile
+  static constexpr int STAGES = C::STAGES;
+  static constexpr int SMEM = 2 * C::TILE_BYTES + STAGES * 2 * KT_BYTES + 1024 + 512;
+  static constexpr int S_COL = 0, DP_COL = 64, DS_COL = 128, DQ_COL = 160;
+  static_assert(DQ_COL + DH <= C::TMEM_COLS, "TMEM budget");
+  static_assert(C::CTAS * (SMEM + 1024) <= 228 * 1024, "shared memory per SM");
+};
+
+template <int DH>
+__global__ void __launch_bounds__(THREADS, BCfg<DH>::CTAS)
+attn_scores_dq_kernel(const __grid_constant__ Params P) {
+  using C = BCfg<DH>;
+  using Q = QCfg<DH>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  uint8_t* sQ = smem;
+  uint8_t* sdO = sQ + C::TILE_BYTES;
+  uint8_t* sK = sdO + C::TILE_BYTES;
+  uint8_t* sV = sK + Q::STAGES * Q::KT_BYTES;
+  uint64_t* bar = reinterpret_cast<uint64_t*>(sV + Q::STAGES * Q::KT_BYTES);
+  uint64_t* q_full = bar;
+  uint64_t* r_full = bar + 1;
+  uint64_t* r_empty = r_full + Q::STAGES;
+  uint64_t* r_clean = r_empty + Q::STAGES;
+  uint64_t* sdp_full = r_clean + Q::STAGES;
+  uint64_t* s_free = sdp_full + 1;
+  uint64_t* d_ready = s_free + 1;
+  uint64_t* d_free = d_ready + 1;
+  uint64_t* acc_full = d_free + 1;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(acc_full + 1);
+  int* sp = reinterpret_cast<int*>(tmem_holder + 4);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const int bs = P.B * P.S;
+  const int qt = P.nq - 1 - blockIdx.x / bs;
+  const int s_idx = blockIdx.x % bs % P.S, b_idx = blockIdx.x % bs / P.S;
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 1);
+    for (int s = 0; s < Q::STAGES; ++s) {
+      mbar_init(&r_full[s], 1);
+      mbar_init(&r_empty[s], 2);  // the product that read it last, and the cleaning warp
+      mbar_init(&r_clean[s], 1);
+    }
+    mbar_init(sdp_full, 1);
+    mbar_init(s_free, 4);
+    mbar_init(d_ready, 4);
+    mbar_init(d_free, 1);
+    mbar_init(acc_full, 1);
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_holder, C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  if (warp == 0 && lane == 0) {
+    prefetch_tmap(&P.tm_q);
+    prefetch_tmap(&P.tm_do);
+    prefetch_tmap(&P.tm_k);
+    prefetch_tmap(&P.tm_v);
+  }
+  pdl_wait();
+  pdl_allow_next();
+  const int row = threadIdx.x & 127;
+  const int q = qt * TQ + row;
+  int b0 = 0, e0 = 0;
+  if (warp >= 4) {
+    span_of(P.span, b_idx, q, b0, e0);
+    const bool live = b0 < e0;
+    const int lo = __reduce_min_sync(0xffffffffu, live ? b0 : INT_MAX);
+    const int hi = __reduce_max_sync(0xffffffffu, live ? e0 : 0);
+    const int blo = __reduce_max_sync(0xffffffffu, live ? b0 : 0);
+    const int ehi = __reduce_min_sync(0xffffffffu, live ? e0 : INT_MAX);
+    if (lane == 0) {
+      int* d = sp + (warp & 3) * 4;
+      d[0] = lo;
+      d[1] = hi;
+      d[2] = blo;
+      d[3] = ehi;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+  const int lo = min(min(sp[0], sp[4]), min(sp[8], sp[12]));
+  const int hi = max(max(sp[1], sp[5]), max(sp[9], sp[13]));
+  const int full_lo = max(max(sp[2], sp[6]), max(sp[10], sp[14]));
+  const int full_hi = min(min(sp[3], sp[7]), min(sp[11], sp[15]));
+  const int j0 = lo < hi ? lo / Q::TKD : 0;
+  const int nk = lo < hi ? (hi + Q::TKD - 1) / Q::TKD - j0 : 0;  // steps j0 .. j0 + nk - 1
+  auto whole = [&](int j) { return j * Q::TKD >= full_lo && (j + 1) * Q::TKD <= full_hi; };
+  const int kvh = s_idx < P.Sr ? s_idx / P.k : 0;
+
+  if (warp < 4) {
+    if constexpr (C::CTAS == 2) setmaxnreg_dec<kSmallRegs>();
+    if (warp == 0) {
+      // ---------------------------------------------------------------- loads
+      if (lane == 0 && nk > 0) {
+        mbar_arrive_expect_tx(q_full, 2 * C::TILE_BYTES);
+        tma_load_5d(sQ, &P.tm_q, 0, qt * TQ, 0, s_idx, b_idx, q_full);
+        tma_load_5d(sdO, &P.tm_do, 0, qt * TQ, 0, s_idx, b_idx, q_full);
+        int st = 0;
+        uint32_t ph = 0;
+        for (int j = 0; j < nk; ++j) {
+          if (!lane_wait(&r_empty[st], ph ^ 1, P)) break;
+          mbar_arrive_expect_tx(&r_full[st], 2 * Q::KT_BYTES);
+          tma_load_5d(sK + st * Q::KT_BYTES, &P.tm_k, 0, (j0 + j) * Q::TKD, 0, kvh, b_idx,
+                      &r_full[st]);
+          tma_load_5d(sV + st * Q::KT_BYTES, &P.tm_v, 0, (j0 + j) * Q::TKD, 0, kvh, b_idx,
+                      &r_full[st]);
+          if (++st == Q::STAGES) {
+            st = 0;
+            ph ^= 1;
+          }
+        }
+      }
+    } else if (warp == 3) {
+      // ---------------------------------------------------------------- cleaning of K tiles
+      int st = 0;
+      uint32_t ph = 0;
+      for (int j = 0; j < nk; ++j) {
+        if (!warp_wait(&r_full[st], ph, P)) break;
+        if (!whole(j0 + j)) {
+          if (clean_tile(sK + st * Q::KT_BYTES, Q::KT_BYTES)) fence_async_shared();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&r_clean[st]);
+        }
+        // every tile passes here, so this warp is never a phase of a stage behind or ahead
+        if (lane == 0) mbar_arrive(&r_empty[st]);
+        if (++st == Q::STAGES) {
+          st = 0;
+          ph ^= 1;
+        }
+      }
+    } else if (warp == 1) {
+      // ---------------------------------------------------------------- MMA issue
+      const uint32_t idesc_s = idesc_bf16_f32(TQ, Q::TKD);
+      const uint32_t idesc_dq = idesc_bf16_f32(TQ, DH) | (1u << 16);  // B (K) MN-major
+      const uint64_t q_desc = smem_desc(smem_u32(sQ), 8 * C::ROW_BYTES, C::LAYOUT);
+      const uint64_t do_desc = smem_desc(smem_u32(sdO), 8 * C::ROW_BYTES, C::LAYOUT);
+      const uint64_t k_desc = smem_desc(smem_u32(sK), 8 * C::ROW_BYTES, C::LAYOUT);
+      const uint64_t v_desc = smem_desc(smem_u32(sV), 8 * C::ROW_BYTES, C::LAYOUT);
+      const uint64_t kmn_desc =
+          smem_desc_mn(smem_u32(sK), Q::TKD * C::ROW_BYTES, 8 * C::ROW_BYTES, C::LAYOUT);
+      constexpr uint32_t kStep = Q::KT_BYTES >> 4;
+      int st_next = 0;
+      uint32_t ph = 0, clean_phase = 0;
+      // S = Q K^T and dP = dO V^T of step j
+      auto issue_sdp = [&](int j) -> bool {
+        if (!warp_wait(&r_full[st_next], ph, P)) return false;
+        if (!whole(j0 + j)) {
+          if (!warp_wait(&r_clean[st_next], (clean_phase >> st_next) & 1, P)) return false;
+          clean_phase ^= 1u << st_next;
+        }
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t kd = k_desc + (uint64_t)(st_next * kStep);
+          const uint64_t vd = v_desc + (uint64_t)(st_next * kStep);
+#pragma unroll
+          for (int kk = 0; kk < DH / 16; ++kk)
+            mma_ss(tmem + Q::S_COL, q_desc + kmajor_off<DH, 128>(kk),
+                   kd + kmajor_off<DH, Q::TKD>(kk), idesc_s, kk > 0 ? 1u : 0u);
+#pragma unroll
+          for (int kk = 0; kk < DH / 16; ++kk)
+            mma_ss(tmem + Q::DP_COL, do_desc + kmajor_off<DH, 128>(kk),
+                   vd + kmajor_off<DH, Q::TKD>(kk), idesc_s, kk > 0 ? 1u : 0u);
+          mma_commit(sdp_full);
+        }
+        __syncwarp();
+        if (++st_next == Q::STAGES) {
+          st_next = 0;
+          ph ^= 1;
+        }
+        return true;
+      };
+      bool ok = nk > 0 && warp_wait(q_full, 0, P) && issue_sdp(0);
+      int st = 0;
+      for (int j = 0; ok && j < nk; ++j) {
+        if (j + 1 < nk) {
+          // the softmax warps hold S(j), dP(j) in registers: the next pair may be written
+          if (!warp_wait(s_free, j & 1, P) || !issue_sdp(j + 1)) break;
+        }
+        if (!warp_wait(d_ready, j & 1, P)) break;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t kd = kmn_desc + (uint64_t)(st * kStep);
+#pragma unroll
+          for (int kk = 0; kk < Q::TKD / 16; ++kk)
+            mma_ts(tmem + Q::DQ_COL, tmem + Q::DS_COL + kk * 8,
+                   kd + (uint64_t)((kk * 16 * C::ROW_BYTES) >> 4), idesc_dq,
+                   (j == 0 && kk == 0) ? 0u : 1u);
+          mma_commit(&r_empty[st]);
+          mma_commit(d_free);
+          if (j + 1 == nk) mma_commit(acc_full);
+        }
+        __syncwarp();
+        if (++st == Q::STAGES) st = 0;
+      }
+    }
+  } else {
+    // ------------------------------------------------------------------ softmax + epilogue
+    if constexpr (C::CTAS == 2) setmaxnreg_inc<kLargeRegs>();
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t t_base = tmem + lane_off;
+    const bool valid = q < P.T, live = b0 < e0;
+    const int64_t tok = (int64_t)b_idx * P.T + q;
+    const int64_t srow = (int64_t)s_idx * P.B * P.T + tok;
+    const float lse = live ? P.lse[srow] : 0.f;
+    const float dsum = live ? P.dsum[srow] : 0.f;
+    const float slope2 = P.slopes ? P.slopes[s_idx] * kLog2e : 0.f;
+    bool ok = true;
+    by_form(P.cap_log2 != 0.f, P.slopes != nullptr, [&](auto cap, auto bias) {
+      constexpr bool CAP = decltype(cap)::value, BIAS = decltype(bias)::value;
+      for (int j = 0; j < nk; ++j) {
+        if (!warp_wait(sdp_full, j & 1, P)) { ok = false; break; }
+        tc_fence_after();
+        const int kv0 = (j0 + j) * Q::TKD;
+        uint32_t pk[32];
+        {
+          uint32_t sr[64], dr[64];
+          tmem_ld64_wait(t_base + Q::S_COL, sr);
+          tmem_ld64_wait(t_base + Q::DP_COL, dr);
+          if (j + 1 < nk) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(s_free);
+          }
+          const float d0 = (float)(kv0 - q);
+          auto one = [&](int c) {
+            float dc;
+            const float z =
+                score<CAP, BIAS>(P, __uint_as_float(sr[c]), slope2, d0 + (float)c, dc);
+            const float v = ex2(z - lse) * (__uint_as_float(dr[c]) - dsum);
+            return CAP ? v * dc : v;
+          };
+          if (whole(j0 + j)) {
+#pragma unroll
+            for (int x = 0; x < 32; ++x) pk[x] = pack_bf16x2(one(2 * x), one(2 * x + 1));
+          } else {
+            const int first = b0 - kv0, last = e0 - kv0;
+#pragma unroll
+            for (int x = 0; x < 32; ++x) {
+              const float v0 = one(2 * x), v1 = one(2 * x + 1);
+              pk[x] = pack_bf16x2(2 * x >= first && 2 * x < last ? v0 : 0.f,
+                                  2 * x + 1 >= first && 2 * x + 1 < last ? v1 : 0.f);
+            }
+          }
+        }
+        // the previous dQ product has read dz: it may be overwritten
+        if (j > 0 && !warp_wait(d_free, (j - 1) & 1, P)) { ok = false; break; }
+#pragma unroll
+        for (int c0 = 0; c0 < 32; c0 += 8) tmem_st8(t_base + Q::DS_COL + c0, pk + c0);
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(d_ready);
+      }
+    });
+    if (ok && nk > 0) ok = warp_wait(acc_full, 0, P);
+    if (ok) {
+      tc_fence_after();
+      __nv_bfloat16* dst = nullptr;
+      if (valid) {
+        if (!P.sel) {
+          dst = P.dq + (int64_t)s_idx * P.dq_hs + tok * P.dq_ts;
+        } else if (s_idx < P.Sr) {
+          const int e = (s_idx / P.k) * P.experts + P.sel[tok * P.sel_stride + P.sel_off + s_idx];
+          dst = P.dq + tok * P.dq_ts + (int64_t)e * DH;
+        } else {
+          dst = P.dq_shared + tok * DH;
+        }
+      }
+      if (nk > 0) store_row<DH>(t_base + Q::DQ_COL, dst, P.scale, valid, !live);
+      else if (valid) zero_row<DH>(dst);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+}
+
+// ---------------------------------------------------------------------------------------
+// dK, dV. Jobs of TQJ queries, small enough that S^T, dP^T, p^T, dz^T, dV and dK all have TMEM
+// columns of their own: at two CTAs per SM (256 columns) 48 queries for head dims up to 48
+// and 32 for 64; at one CTA per SM (512 columns) 64.
+// ---------------------------------------------------------------------------------------
+template <int DH>
+struct KCfg {
+  using C = BCfg<DH>;
+  static constexpr int TQJ = DH <= 48 ? 48 : (DH <= 64 ? 32 : 64);
+  static constexpr int QT_BYTES = TQJ * DH * 2;
+  static constexpr int STAGES = C::STAGES;
+  // per softmax warp: two buffers of a job's lse, D, first keys and ends of keys
+  static constexpr int WARP_STAGE = 4 * 2 * 4 * TQJ * 4;
+  static constexpr int SMEM = 2 * C::TILE_BYTES + STAGES * 2 * QT_BYTES + 1024 + 512 + WARP_STAGE;
+  static constexpr int S_COL = 0, DP_COL = TQJ, P_COL = 2 * TQJ, DS_COL = 2 * TQJ + TQJ / 2;
+  static constexpr int DV_COL = 3 * TQJ, DK_COL = 3 * TQJ + DH;
+  static_assert(TQJ % 16 == 0 && TQJ <= 64, "a job's queries: two per lane at most");
+  static_assert(DK_COL + DH <= C::TMEM_COLS, "TMEM budget");
+  static_assert(C::CTAS * (SMEM + 1024) <= 228 * 1024, "shared memory per SM");
+};
+
+template <int DH>
+__global__ void __launch_bounds__(THREADS, BCfg<DH>::CTAS)
+attn_scores_dkdv_kernel(const __grid_constant__ Params P) {
+  using C = BCfg<DH>;
+  using K = KCfg<DH>;
+  constexpr int TQJ = K::TQJ;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  uint8_t* sK = smem;
+  uint8_t* sV = sK + C::TILE_BYTES;
+  uint8_t* sQ = sV + C::TILE_BYTES;
+  uint8_t* sdO = sQ + K::STAGES * K::QT_BYTES;
+  float* wstage = reinterpret_cast<float*>(sdO + K::STAGES * K::QT_BYTES);
+  uint64_t* bar = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(wstage) + K::WARP_STAGE);
+  uint64_t* kv_full = bar;
+  uint64_t* r_full = bar + 1;
+  uint64_t* r_empty = r_full + K::STAGES;
+  uint64_t* r_clean = r_empty + K::STAGES;
+  uint64_t* sdp_full = r_clean + K::STAGES;
+  uint64_t* s_free = sdp_full + 1;
+  uint64_t* d_ready = s_free + 1;
+  uint64_t* d_free = d_ready + 1;
+  uint64_t* acc_full = d_free + 1;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(acc_full + 1);
+  int* sp = reinterpret_cast<int*>(tmem_holder + 4);
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  // first key tiles first: under a causal mask the most queries see them
+  const int bg = P.B * P.G;
+  const int kt = blockIdx.x / bg, g = blockIdx.x % bg % P.G, b_idx = blockIdx.x % bg / P.G;
+  const int u0 = kt * TK, u1 = min(u0 + TK, P.T);
+  if (threadIdx.x == 0) {
+    mbar_init(kv_full, 1);
+    for (int s = 0; s < K::STAGES; ++s) {
+      mbar_init(&r_full[s], 1);
+      mbar_init(&r_empty[s], 1);
+      mbar_init(&r_clean[s], 1);
+    }
+    mbar_init(sdp_full, 1);
+    mbar_init(s_free, 4);
+    mbar_init(d_ready, 4);
+    mbar_init(d_free, 1);
+    mbar_init(acc_full, 1);
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_holder, C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  if (warp == 0 && lane == 0) {
+    prefetch_tmap(&P.tm_q);
+    prefetch_tmap(&P.tm_do);
+    prefetch_tmap(&P.tm_k);
+    prefetch_tmap(&P.tm_v);
+  }
+  pdl_wait();
+  pdl_allow_next();
+  // the 128-row blocks of queries that may see a key of this tile: first .. last
+  int first = INT_MAX, last = -1;
+  if (P.blocks) {
+    for (int i = threadIdx.x; i < P.nq; i += THREADS) {
+      const int2 v = P.blocks[(int64_t)b_idx * P.nq + i];
+      if (v.x < u1 && v.y > u0) {
+        first = min(first, i);
+        last = max(last, i);
+      }
+    }
+    first = __reduce_min_sync(0xffffffffu, first);
+    last = __reduce_max_sync(0xffffffffu, last);
+    if (lane == 0) {
+      sp[2 * warp] = first;
+      sp[2 * warp + 1] = last;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+  int q_lo = P.span.causal ? u0 : 0, q_hi = P.T;  // queries q_lo .. q_hi - 1
+  if (P.blocks) {
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; ++w) {
+      first = min(first, sp[2 * w]);
+      last = max(last, sp[2 * w + 1]);
+    }
+    q_lo = last >= 0 ? first * D_ROWS : 0;
+    q_hi = last >= 0 ? min(P.T, (last + 1) * D_ROWS) : 0;
+  }
+  const int qt0 = q_lo / TQJ;
+  const int per = q_lo < q_hi ? (q_hi + TQJ - 1) / TQJ - qt0 : 0;  // query tiles of a stream
+  const int ns = P.k + (g == 0 && P.S > P.Sr ? 1 : 0);             // streams of the head
+  const int nj = ns * per;
+  auto stream_of = [&](int si) { return si < P.k ? g * P.k + si : P.Sr; };
+  // Whether every query of a job sees every key of the tile; lane l holds the intervals of
+  // queries l and l + 32 of the job.
+  auto job_spans = [&](int qt, int (&jb)[2], int (&je)[2]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      jb[h] = 0;
+      je[h] = 0;
+      if (lane + 32 * h < TQJ) span_of(P.span, b_idx, qt * TQJ + lane + 32 * h, jb[h], je[h]);
+    }
+  };
+  auto whole = [&](const int (&jb)[2], const int (&je)[2]) {
+    bool w = jb[0] <= u0 && je[0] >= u1;
+    if (lane + 32 < TQJ) w = w && jb[1] <= u0 && je[1] >= u1;
+    return __all_sync(0xffffffffu, w) != 0;
+  };
+
+  if (warp < 4) {
+    if constexpr (C::CTAS == 2) setmaxnreg_dec<kSmallRegs>();
+    if (warp == 0) {
+      // ---------------------------------------------------------------- loads
+      if (lane == 0 && nj > 0) {
+        mbar_arrive_expect_tx(kv_full, 2 * C::TILE_BYTES);
+        tma_load_5d(sK, &P.tm_k, 0, u0, 0, g, b_idx, kv_full);
+        tma_load_5d(sV, &P.tm_v, 0, u0, 0, g, b_idx, kv_full);
+        int st = 0, si = 0, r = 0;
+        uint32_t ph = 0;
+        for (int j = 0; j < nj; ++j) {
+          if (!lane_wait(&r_empty[st], ph ^ 1, P)) break;
+          mbar_arrive_expect_tx(&r_full[st], 2 * K::QT_BYTES);
+          const int s = stream_of(si), qrow = (qt0 + r) * TQJ;
+          tma_load_5d(sQ + st * K::QT_BYTES, &P.tm_q, 0, qrow, 0, s, b_idx, &r_full[st]);
+          tma_load_5d(sdO + st * K::QT_BYTES, &P.tm_do, 0, qrow, 0, s, b_idx, &r_full[st]);
+          if (++r == per) {
+            r = 0;
+            ++si;
+          }
+          if (++st == K::STAGES) {
+            st = 0;
+            ph ^= 1;
+          }
+        }
+      }
+    } else if (warp == 3) {
+      // ------------------------------------------ cleaning of the q and dout tiles of jobs
+      // that are seen in part; passes every job on to the MMA warp
+      int st = 0, r = 0;
+      uint32_t ph = 0;
+      int jb[2], je[2];
+      job_spans(qt0, jb, je);
+      for (int j = 0; j < nj; ++j) {
+        const bool w = whole(jb, je);
+        if (++r == per) r = 0;
+        if (j + 1 < nj) job_spans(qt0 + r, jb, je);
+        if (!warp_wait(&r_full[st], ph, P)) break;
+        if (!w) {
+          const bool bq = clean_tile(sQ + st * K::QT_BYTES, K::QT_BYTES);
+          const bool bd = clean_tile(sdO + st * K::QT_BYTES, K::QT_BYTES);
+          if (bq || bd) fence_async_shared();
+          __syncwarp();
+        }
+        if (lane == 0) mbar_arrive(&r_clean[st]);
+        if (++st == K::STAGES) {
+          st = 0;
+          ph ^= 1;
+        }
+      }
+    } else if (warp == 1) {
+      // ---------------------------------------------------------------- MMA issue
+      const uint32_t idesc_s = idesc_bf16_f32(TK, TQJ);
+      const uint32_t idesc_kv = idesc_bf16_f32(TK, DH) | (1u << 16);  // B (Q, dO) MN-major
+      const uint64_t k_desc = smem_desc(smem_u32(sK), 8 * C::ROW_BYTES, C::LAYOUT);
+      const uint64_t v_desc = smem_desc(smem_u32(sV), 8 * C::ROW_BYTES, C::LAYOUT);
+      const uint64_t q_desc = smem_desc(smem_u32(sQ), 8 * C::ROW_BYTES, C::LAYOUT);
+      const uint64_t do_desc = smem_desc(smem_u32(sdO), 8 * C::ROW_BYTES, C::LAYOUT);
+      const uint64_t qmn_desc =
+          smem_desc_mn(smem_u32(sQ), TQJ * C::ROW_BYTES, 8 * C::ROW_BYTES, C::LAYOUT);
+      const uint64_t domn_desc =
+          smem_desc_mn(smem_u32(sdO), TQJ * C::ROW_BYTES, 8 * C::ROW_BYTES, C::LAYOUT);
+      constexpr uint32_t kStep = K::QT_BYTES >> 4;
+      int st_next = 0;
+      uint32_t ph = 0;
+      // S^T = K Q^T and dP^T = V dO^T of the next job
+      auto issue_sdp = [&]() -> bool {
+        if (!warp_wait(&r_full[st_next], ph, P) || !warp_wait(&r_clean[st_next], ph, P))
+          return false;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t qd = q_desc + (uint64_t)(st_next * kStep);
+          const uint64_t dd = do_desc + (uint64_t)(st_next * kStep);
+#pragma unroll
+          for (int kk = 0; kk < DH / 16; ++kk)
+            mma_ss(tmem + K::S_COL, k_desc + kmajor_off<DH, 128>(kk), qd + kmajor_off<DH, TQJ>(kk),
+                   idesc_s, kk > 0 ? 1u : 0u);
+#pragma unroll
+          for (int kk = 0; kk < DH / 16; ++kk)
+            mma_ss(tmem + K::DP_COL, v_desc + kmajor_off<DH, 128>(kk),
+                   dd + kmajor_off<DH, TQJ>(kk), idesc_s, kk > 0 ? 1u : 0u);
+          mma_commit(sdp_full);
+        }
+        __syncwarp();
+        if (++st_next == K::STAGES) {
+          st_next = 0;
+          ph ^= 1;
+        }
+        return true;
+      };
+      bool ok = nj > 0 && warp_wait(kv_full, 0, P) && issue_sdp();
+      int st = 0;
+      for (int j = 0; ok && j < nj; ++j) {
+        if (j + 1 < nj) {
+          if (!warp_wait(s_free, j & 1, P) || !issue_sdp()) break;
+        }
+        if (!warp_wait(d_ready, j & 1, P)) break;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t dmn = domn_desc + (uint64_t)(st * kStep);
+          const uint64_t qmn = qmn_desc + (uint64_t)(st * kStep);
+#pragma unroll
+          for (int kk = 0; kk < TQJ / 16; ++kk)
+            mma_ts(tmem + K::DV_COL, tmem + K::P_COL + kk * 8,
+                   dmn + (uint64_t)((kk * 16 * C::ROW_BYTES) >> 4), idesc_kv,
+                   (j == 0 && kk == 0) ? 0u : 1u);
+#pragma unroll
+          for (int kk = 0; kk < TQJ / 16; ++kk)
+            mma_ts(tmem + K::DK_COL, tmem + K::DS_COL + kk * 8,
+                   qmn + (uint64_t)((kk * 16 * C::ROW_BYTES) >> 4), idesc_kv,
+                   (j == 0 && kk == 0) ? 0u : 1u);
+          mma_commit(&r_empty[st]);
+          mma_commit(d_free);
+          if (j + 1 == nj) mma_commit(acc_full);
+        }
+        __syncwarp();
+        if (++st == K::STAGES) st = 0;
+      }
+    }
+  } else {
+    // ------------------------------------------------------------------ softmax + epilogue
+    if constexpr (C::CTAS == 2) setmaxnreg_inc<kLargeRegs>();
+    const int row = (warp & 3) * 32 + lane;  // key row of the tile
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t t_base = tmem + lane_off;
+    float* wL = wstage + (warp & 3) * (2 * 4 * TQJ);  // [2][4][TQJ]: lse, D, first, end
+    const int u = u0 + row;
+    const bool key_ok = u < P.T;
+    bool ok = true;
+    // a job's lse, D and intervals: lane l loads queries l and l + 32, one job ahead
+    float nl[2], nd[2];
+    int jb[2], je[2];
+    auto fetch = [&](int si, int qt) {
+      job_spans(qt, jb, je);
+      const int64_t base = (int64_t)stream_of(si) * P.B * P.T + (int64_t)b_idx * P.T;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const bool live = jb[h] < je[h];  // false for queries past the sequence
+        nl[h] = live ? P.lse[base + qt * TQJ + lane + 32 * h] : 0.f;
+        nd[h] = live ? P.dsum[base + qt * TQJ + lane + 32 * h] : 0.f;
+      }
+    };
+    if (nj > 0) fetch(0, qt0);
+    by_form(P.cap_log2 != 0.f, P.slopes != nullptr, [&](auto cap, auto bias) {
+      constexpr bool CAP = decltype(cap)::value, BIAS = decltype(bias)::value;
+      int si = 0, r = 0;
+      for (int j = 0; j < nj; ++j) {
+        float* sL = wL + (j & 1) * 4 * TQJ;
+        float* sD = sL + TQJ;
+        int* sB = reinterpret_cast<int*>(sD + TQJ);
+        int* sE = sB + TQJ;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int c = lane + 32 * h;
+          if (c < TQJ) {
+            sL[c] = nl[h];
+            sD[c] = nd[h];
+            sB[c] = jb[h];
+            sE[c] = je[h];
+          }
+        }
+        const bool all_live = whole(jb, je);
+        __syncwarp();  // this warp's buffer is complete (the other is two jobs old)
+        const float slope2 = BIAS ? P.slopes[stream_of(si)] * kLog2e : 0.f;
+        const float d0 = (float)((qt0 + r) * TQJ - u);
+        if (++r == per) {
+          r = 0;
+          ++si;
+        }
+        if (j + 1 < nj) fetch(si, qt0 + r);
+        if (!warp_wait(sdp_full, j & 1, P)) { ok = false; break; }
+        tc_fence_after();
+        uint32_t pp[TQJ / 2], pd[TQJ / 2];
+        {
+          uint32_t sr[TQJ], dr[TQJ];
+          tmem_ldN_wait<TQJ>(t_base + K::S_COL, sr);
+          tmem_ldN_wait<TQJ>(t_base + K::DP_COL, dr);
+          if (j + 1 < nj) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(s_free);
+          }
+          auto one = [&](int c, float L, float D, float& p, float& d) {
+            float dc;
+            const float z =
+                score<CAP, BIAS>(P, __uint_as_float(sr[c]), slope2, d0 + (float)c, dc);
+            p = ex2(z - L);
+            d = p * (__uint_as_float(dr[c]) - D);
+            if (CAP) d *= dc;
+          };
+          if (all_live) {
+#pragma unroll
+            for (int x4 = 0; x4 < TQJ / 4; ++x4) {
+              const float4 L4 = reinterpret_cast<const float4*>(sL)[x4];
+              const float4 D4 = reinterpret_cast<const float4*>(sD)[x4];
+              float p[4], d[4];
+              one(4 * x4, L4.x, D4.x, p[0], d[0]);
+              one(4 * x4 + 1, L4.y, D4.y, p[1], d[1]);
+              one(4 * x4 + 2, L4.z, D4.z, p[2], d[2]);
+              one(4 * x4 + 3, L4.w, D4.w, p[3], d[3]);
+              pp[2 * x4] = pack_bf16x2(p[0], p[1]);
+              pp[2 * x4 + 1] = pack_bf16x2(p[2], p[3]);
+              pd[2 * x4] = pack_bf16x2(d[0], d[1]);
+              pd[2 * x4 + 1] = pack_bf16x2(d[2], d[3]);
+            }
+          } else {
+#pragma unroll
+            for (int x = 0; x < TQJ / 2; ++x) {
+              float p[2], d[2];
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const int c = 2 * x + e;
+                const float D = sD[c];
+                one(c, sL[c], D, p[e], d[e]);
+                // a row whose dout was cleaned has an infinite or NaN D, which p takes on
+                p[e] = fmaf(0.f, D, p[e]);
+                const bool in = key_ok && u >= sB[c] && u < sE[c];
+                p[e] = in ? p[e] : 0.f;
+                d[e] = in ? d[e] : 0.f;
+              }
+              pp[x] = pack_bf16x2(p[0], p[1]);
+              pd[x] = pack_bf16x2(d[0], d[1]);
+            }
+          }
+        }
+        // the previous job's products have read p^T and dz^T
+        if (j > 0 && !warp_wait(d_free, (j - 1) & 1, P)) { ok = false; break; }
+#pragma unroll
+        for (int c0 = 0; c0 < TQJ / 2; c0 += 8) {
+          tmem_st8(t_base + K::P_COL + c0, pp + c0);
+          tmem_st8(t_base + K::DS_COL + c0, pd + c0);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(d_ready);
+      }
+    });
+    if (ok && nj > 0) ok = warp_wait(acc_full, 0, P);
+    if (ok) {
+      tc_fence_after();
+      const int64_t tok = (int64_t)b_idx * P.T + u;
+      __nv_bfloat16* dk = P.dk + (int64_t)g * P.dk_hs + tok * P.dk_ts;
+      __nv_bfloat16* dv = P.dv + (int64_t)g * P.dv_hs + tok * P.dv_ts;
+      if (nj > 0) {
+        store_row<DH>(t_base + K::DK_COL, dk, P.scale, key_ok, false);
+        store_row<DH>(t_base + K::DV_COL, dv, 1.f, key_ok, false);
+      } else if (key_ok) {
+        zero_row<DH>(dk);
+        zero_row<DH>(dv);
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+}
+
+template <int DH>
+int launch_dh(const AttnArgs& a, cudaStream_t st) {
+  using C = BCfg<DH>;
+  using Q = QCfg<DH>;
+  using K = KCfg<DH>;
+  if (!set_smem_limit_once<attn_scores_dq_kernel<DH>>(Q::SMEM)) return -1;
+  if (!set_smem_limit_once<attn_scores_dkdv_kernel<DH>>(K::SMEM)) return -1;
+  const CUtensorMapSwizzle sw = C::CW == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_32B;
+  Params P;
+  memset(&P, 0, sizeof(P));
+  P.span = SpanArgs{a.key_begin, a.key_end, a.T, a.causal};
+  P.lse = a.lse;
+  P.dsum = a.dsum;
+  P.slopes = a.slopes;
+  const bool masked = a.key_begin || a.key_end;
+  P.blocks = masked ? a.blocks : nullptr;
+  P.dq = static_cast<__nv_bfloat16*>(a.dq.data);
+  P.dk = static_cast<__nv_bfloat16*>(a.dk.data);
+  P.dv = static_cast<__nv_bfloat16*>(a.dv.data);
+  P.dq_hs = a.dq.head_stride;
+  P.dq_ts = a.dq.token_stride;
+  P.dk_hs = a.dk.head_stride;
+  P.dk_ts = a.dk.token_stride;
+  P.dv_hs = a.dv.head_stride;
+  P.dv_ts = a.dv.token_stride;
+  P.sel = a.sel;
+  P.dq_shared = static_cast<__nv_bfloat16*>(a.dq_shared);
+  P.sel_stride = a.sel_stride;
+  P.sel_off = a.sel_off;
+  P.experts = a.experts;
+  P.T = a.T;
+  P.B = a.B;
+  P.S = a.S;
+  P.Sr = a.G * a.k;
+  P.k = a.k;
+  P.G = a.G;
+  P.nq = (a.T + TQ - 1) / TQ;
+  P.scale = a.scale;
+  P.scale_log2 = a.scale * kLog2e;
+  P.cap_in = a.softcap > 0.f ? 2.f * a.scale * kLog2e / a.softcap : 0.f;
+  P.cap_log2 = a.softcap * kLog2e;
+  P.status = a.status;
+  P.spin = a.spin > 0 ? a.spin : (int64_t)1 << 22;
+  int n = 0;
+  if (!a.dsum_given || masked) {
+    const dim3 grid((unsigned)(a.B * (int64_t)P.nq), a.dsum_given ? 1 : a.S);
+    if (launch_pdl(attn_scores_d_kernel<DH>, grid, dim3(THREADS), 0, st, a.dout, a.out, a.dsum,
+                   masked ? a.blocks : nullptr, P.span, a.B, P.nq, a.dsum_given) != cudaSuccess)
+      return -1;
+    ++n;
+  }
+  if (!tmap_heads(&P.tm_q, a.q, a.B, a.T, DH, C::CW, TQ, sw) ||
+      !tmap_heads(&P.tm_do, a.dout, a.B, a.T, DH, C::CW, TQ, sw) ||
+      !tmap_heads(&P.tm_k, a.kk, a.B, a.T, DH, C::CW, Q::TKD, sw) ||
+      !tmap_heads(&P.tm_v, a.v, a.B, a.T, DH, C::CW, Q::TKD, sw))
+    return -1;
+  if (launch_pdl(attn_scores_dq_kernel<DH>, dim3((unsigned)((int64_t)a.B * a.S * P.nq)),
+                 dim3(THREADS), Q::SMEM, st, P) != cudaSuccess)
+    return -1;
+  ++n;
+  if (!tmap_heads(&P.tm_q, a.q, a.B, a.T, DH, C::CW, K::TQJ, sw) ||
+      !tmap_heads(&P.tm_do, a.dout, a.B, a.T, DH, C::CW, K::TQJ, sw) ||
+      !tmap_heads(&P.tm_k, a.kk, a.B, a.T, DH, C::CW, TK, sw) ||
+      !tmap_heads(&P.tm_v, a.v, a.B, a.T, DH, C::CW, TK, sw))
+    return -1;
+  if (launch_pdl(attn_scores_dkdv_kernel<DH>, dim3((unsigned)((int64_t)a.B * a.G * P.nq)),
+                 dim3(THREADS), K::SMEM, st, P) != cudaSuccess)
+    return -1;
+  return n + 1;
+}
+
+}  // namespace
+
+int launch_attn_scores_backward(const AttnArgs& a, cudaStream_t st) {
+  switch (a.d_h) {
+    case 16: return launch_dh<16>(a, st);
+    case 32: return launch_dh<32>(a, st);
+    case 48: return launch_dh<48>(a, st);
+    case 64: return launch_dh<64>(a, st);
+    case 80: return launch_dh<80>(a, st);
+    case 96: return launch_dh<96>(a, st);
+    case 112: return launch_dh<112>(a, st);
+    case 128: return launch_dh<128>(a, st);
+    default: return -1;
+  }
+}
+
+}  // namespace gqe

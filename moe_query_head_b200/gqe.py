@@ -25,7 +25,11 @@ EXPORTED = ("gqe_create", "gqe_forward", "gqe_get_routing", "gqe_get_tensor",
             "gqe_workspace_bytes", "gqe_kernel_launches", "gqe_set_stage_events",
             "gqe_stage_name", "gqe_route_static", "gqe_exp2_fma", "gqe_selftest_timeout",
             "gqe_decode", "gqe_enable_backward", "gqe_backward", "gqe_backward_launches",
-            "gqe_set_group_range", "gqe_backward_begin", "gqe_backward_finish")
+            "gqe_set_group_range", "gqe_backward_begin", "gqe_backward_finish",
+            "gqe_qk_norm_rope", "gqe_qk_norm_rope_workspace_bytes", "gqe_qk_norm_rope_backward",
+            "gqe_qk_norm_rope_append", "gqe_attention_forward", "gqe_attention_workspace_bytes",
+            "gqe_attention_backward", "gqe_attention_decode_workspace_bytes",
+            "gqe_attention_decode", "gqe_check_op_status")
 GQE_NUM_STAGES = 6
 
 
@@ -33,6 +37,29 @@ class GQEError(RuntimeError):
     def __init__(self, status: int, where: str):
         super().__init__(f"{where}: {status_str(status)}")
         self.status = status
+
+
+class Heads(ctypes.Structure):
+    """gqe_heads: a [heads, tokens, d_h] tensor by its strides."""
+    _fields_ = [("data", ctypes.c_void_p), ("heads", ctypes.c_int),
+                ("head_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64)]
+
+
+class QkTransform(ctypes.Structure):
+    """gqe_qk_transform."""
+    _fields_ = [("d_h", ctypes.c_int), ("dtype", ctypes.c_int), ("norm", ctypes.c_int),
+                ("eps", ctypes.c_float), ("q_weight", ctypes.c_void_p),
+                ("k_weight", ctypes.c_void_p), ("rot_dim", ctypes.c_int),
+                ("interleaved", ctypes.c_int), ("inv_freq", ctypes.c_void_p)]
+
+
+class Scores(ctypes.Structure):
+    """gqe_scores."""
+    _fields_ = [("B", ctypes.c_int), ("T", ctypes.c_int), ("G", ctypes.c_int),
+                ("k", ctypes.c_int), ("S", ctypes.c_int), ("d_h", ctypes.c_int),
+                ("causal", ctypes.c_int), ("scale", ctypes.c_float), ("softcap", ctypes.c_float),
+                ("slopes", ctypes.c_void_p), ("key_begin", ctypes.c_void_p),
+                ("key_end", ctypes.c_void_p)]
 
 
 def _load() -> ctypes.CDLL:
@@ -88,6 +115,26 @@ def _load() -> ctypes.CDLL:
     lib.gqe_backward_finish.restype = I
     lib.gqe_backward_launches.argtypes = [P]
     lib.gqe_backward_launches.restype = I
+    lib.gqe_qk_norm_rope.argtypes = [P, I, P, P, P, I, P, P, P]
+    lib.gqe_qk_norm_rope.restype = I
+    lib.gqe_qk_norm_rope_workspace_bytes.argtypes = [I]
+    lib.gqe_qk_norm_rope_workspace_bytes.restype = I64
+    lib.gqe_qk_norm_rope_backward.argtypes = [P, I, P, P, P, I, P, P, P, P, P, P, P, SZ, P]
+    lib.gqe_qk_norm_rope_backward.restype = I
+    lib.gqe_qk_norm_rope_append.argtypes = [P, I, P, P, P, P, I, P, P, P, P]
+    lib.gqe_qk_norm_rope_append.restype = I
+    lib.gqe_attention_forward.argtypes = [P, P, P, P, P, P, P]
+    lib.gqe_attention_forward.restype = I
+    lib.gqe_attention_workspace_bytes.argtypes = [P]
+    lib.gqe_attention_workspace_bytes.restype = I64
+    lib.gqe_attention_backward.argtypes = [P, P, P, P, P, P, P, P, P, P, P, SZ, P]
+    lib.gqe_attention_backward.restype = I
+    lib.gqe_attention_decode_workspace_bytes.argtypes = [P, I]
+    lib.gqe_attention_decode_workspace_bytes.restype = I64
+    lib.gqe_attention_decode.argtypes = [P, P, P, P, I, P, P, P, SZ, P]
+    lib.gqe_attention_decode.restype = I
+    lib.gqe_check_op_status.argtypes = [P]
+    lib.gqe_check_op_status.restype = I
     return lib
 
 
@@ -243,3 +290,239 @@ def gqe_set_stage_events(h, events) -> None:
         return
     arr = (ctypes.c_void_p * len(events))(*[ctypes.c_void_p(e.cuda_event) for e in events])
     _check(lib.gqe_set_stage_events(h, arr, len(events)), "gqe_set_stage_events")
+
+
+# ----------------------------------------------------------------------------------------
+# Operators on the layer's streams, without a handle. Tensors are [heads, tokens, d_h] views
+# with dense rows (any head and token strides that are multiples of 16 bytes); sizes, types
+# and devices are checked here, the rest by the library. Calls run on the tensors' device, on
+# `stream` or that device's current stream.
+# ----------------------------------------------------------------------------------------
+_DTYPES = {torch.bfloat16: GQE_BF16, torch.float32: GQE_F32}
+
+
+def _require(ok: bool, where: str) -> None:
+    if not ok:
+        raise GQEError(GQE_ERR_INVALID_ARG, where)
+
+
+def _heads(t, shape, dtype, device, where: str) -> Heads:
+    """The gqe_heads of a tensor of this shape, type and device with dense rows."""
+    st = t.stride()
+    if (t.shape != shape or t.dtype is not dtype or t.device != device
+            or (st[2] != 1 and t.numel())):
+        raise GQEError(GQE_ERR_INVALID_ARG, where)
+    return Heads(t.data_ptr(), shape[0], st[0], st[1])
+
+
+def _cache(t, shape, device, dtype, where: str) -> Heads:
+    """The gqe_heads of a KV cache [G, B, L_max, d_h] with dense rows."""
+    st = t.stride()
+    if (t.shape != shape or t.dtype is not dtype or t.device != device
+            or (t.numel() and (st[3] != 1 or (shape[2] > 1 and st[2] != shape[3])))):
+        raise GQEError(GQE_ERR_INVALID_ARG, where)
+    return Heads(t.data_ptr(), shape[0], st[0], st[1])
+
+
+def _vector(t, n, dtype, device, where: str):
+    """Address of a dense vector of n values, or None."""
+    if t is None:
+        return None
+    if t.numel() != n or t.dtype is not dtype or t.device != device or not t.is_contiguous():
+        raise GQEError(GQE_ERR_INVALID_ARG, where)
+    return t.data_ptr()
+
+
+class _On:
+    """The device of a call's tensors made current, and its stream."""
+
+    def __init__(self, device, stream, where):
+        _require(device.type == "cuda", where)
+        self.device = device
+        self.before = torch.cuda.current_device()
+        self.raw = (stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream
+
+    def __enter__(self):
+        if self.device.index != self.before:
+            torch.cuda.set_device(self.device)
+        return self.raw
+
+    def __exit__(self, *exc):
+        if self.device.index != self.before:
+            torch.cuda.set_device(self.before)
+        return False
+
+
+def _transform(q, norm, q_weight, k_weight, eps, inv_freq, interleaved, where) -> QkTransform:
+    _require(q.dim() == 3 and q.dtype in _DTYPES, where)
+    d, dev = q.shape[2], q.device
+    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
+    return QkTransform(d, _DTYPES[q.dtype], int(norm), eps,
+                       _vector(q_weight, d, torch.float32, dev, where),
+                       _vector(k_weight, d, torch.float32, dev, where), rot, int(interleaved),
+                       _vector(inv_freq, rot // 2, torch.float64, dev, where))
+
+
+def gqe_qk_norm_rope(q, k, q_out, k_out, *, positions=None, T=0, norm=True, q_weight=None,
+                     k_weight=None, eps=1e-6, inv_freq=None, interleaved=False,
+                     stream=None) -> None:
+    """RMS norm of every head of q [Hq, M, d_h] and k [Hk, M, d_h] and rotation by position in
+    one pass (see include/gqe.h). positions: int32 [M], or None for t % T (T = 0: t)."""
+    w = "gqe_qk_norm_rope"
+    tr = _transform(q, norm, q_weight, k_weight, eps, inv_freq, interleaved, w)
+    dt, dev, sq, M = q.dtype, q.device, q.shape, q.shape[1]
+    sk = torch.Size((k.shape[0], M, sq[2]))
+    hq, hk = _heads(q, sq, dt, dev, w), _heads(k, sk, dt, dev, w)
+    oq, ok = _heads(q_out, sq, dt, dev, w), _heads(k_out, sk, dt, dev, w)
+    pos = _vector(positions, M, torch.int32, dev, w)
+    ref = ctypes.byref
+    with _On(dev, stream, w) as st:
+        _check(lib.gqe_qk_norm_rope(ref(tr), M, ref(hq), ref(hk), pos, T or max(M, 1), ref(oq),
+                                    ref(ok), st), w)
+
+
+def gqe_qk_norm_rope_backward(q, k, dq_out, dk_out, dq, dk, dq_weight=None, dk_weight=None, *,
+                              positions=None, T=0, norm=True, q_weight=None, k_weight=None,
+                              eps=1e-6, inv_freq=None, interleaved=False, workspace=None,
+                              stream=None) -> None:
+    """Gradients of gqe_qk_norm_rope given its inputs and the gradients of its outputs (see
+    include/gqe.h); dq_weight, dk_weight: float32 [d_h] to fill, or None."""
+    w = "gqe_qk_norm_rope_backward"
+    tr = _transform(q, norm, q_weight, k_weight, eps, inv_freq, interleaved, w)
+    dt, dev, sq, M = q.dtype, q.device, q.shape, q.shape[1]
+    sk = torch.Size((k.shape[0], M, sq[2]))
+    hq, hk = _heads(q, sq, dt, dev, w), _heads(k, sk, dt, dev, w)
+    gq, gk = _heads(dq_out, sq, dt, dev, w), _heads(dk_out, sk, dt, dev, w)
+    oq, ok = _heads(dq, sq, dt, dev, w), _heads(dk, sk, dt, dev, w)
+    pos = _vector(positions, M, torch.int32, dev, w)
+    wq = _vector(dq_weight, sq[2], torch.float32, dev, w)
+    wk = _vector(dk_weight, sq[2], torch.float32, dev, w)
+    ref = ctypes.byref
+    with _On(dev, stream, w) as st:
+        if workspace is None and norm and (wq or wk):
+            n = max(0, lib.gqe_qk_norm_rope_workspace_bytes(sq[2]))
+            workspace = _scratch(n, dev, stream)
+        _check(lib.gqe_qk_norm_rope_backward(
+            ref(tr), M, ref(hq), ref(hk), pos, T or max(M, 1), ref(gq), ref(gk), ref(oq),
+            ref(ok), wq, wk, *_room(workspace, dev, w), st), w)
+
+
+def _scratch(n: int, device, stream):
+    """n bytes from torch's allocator, in order with the call's stream."""
+    if stream is None:
+        return torch.empty(n, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def _room(workspace, device, where: str):
+    if workspace is None:
+        return None, 0
+    _require(workspace.device == device and workspace.is_contiguous(), where)
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def gqe_qk_norm_rope_append(q, k, v, lengths, q_out, k_cache, v_cache, *, norm=True,
+                            q_weight=None, k_weight=None, eps=1e-6, inv_freq=None,
+                            interleaved=False, stream=None) -> None:
+    """The serving form: q [Hq, B, d_h], k, v [G, B, d_h] of one new token per sequence at
+    positions `lengths` (int32 [B]; -1: idle slot); k and v go to row lengths[b] of the caches
+    [G, B, L_max, d_h] (see include/gqe.h)."""
+    w = "gqe_qk_norm_rope_append"
+    tr = _transform(q, norm, q_weight, k_weight, eps, inv_freq, interleaved, w)
+    _require(k_cache.dim() == 4, w)
+    dt, dev, sq, B = q.dtype, q.device, q.shape, q.shape[1]
+    G, L = k.shape[0], k_cache.shape[2]
+    sk = torch.Size((G, B, sq[2]))
+    sc = torch.Size((G, B, L, sq[2]))
+    hq, hk, hv = _heads(q, sq, dt, dev, w), _heads(k, sk, dt, dev, w), _heads(v, sk, dt, dev, w)
+    oq = _heads(q_out, sq, dt, dev, w)
+    ck, cv = _cache(k_cache, sc, dev, dt, w), _cache(v_cache, sc, dev, dt, w)
+    pos = _vector(lengths, B, torch.int32, dev, w)
+    ref = ctypes.byref
+    with _On(dev, stream, w) as st:
+        _check(lib.gqe_qk_norm_rope_append(ref(tr), B, ref(hq), ref(hk), ref(hv), pos, L, ref(oq),
+                                           ref(ck), ref(cv), st), w)
+
+
+def _scores(q, G, B, T, top_k, causal, scale, softcap, slopes, key_begin, key_end, rows, where):
+    S, dev = q.shape[0], q.device
+    return Scores(B, T, G, top_k, S, q.shape[2], int(causal), scale, softcap,
+                  _vector(slopes, S, torch.float32, dev, where),
+                  _vector(key_begin, rows, torch.int32, dev, where),
+                  _vector(key_end, rows, torch.int32, dev, where))
+
+
+def gqe_attention_forward(q, k, v, out, lse, B, T, top_k, *, causal=True, scale=0.0, softcap=0.0,
+                          slopes=None, key_begin=None, key_end=None, stream=None) -> None:
+    """Attention of the streams q [S, B T, d_h] over k, v [G, B T, d_h] (S = G top_k, or
+    G top_k + 1 with the shared stream) with capped, biased and masked scores; lse: float32
+    [S, B T] to fill for the backward pass, or None (see include/gqe.h)."""
+    w = "gqe_attention_forward"
+    _require(q.dim() == 3 and k.dim() == 3, w)
+    dev, sq, bf = q.device, q.shape, torch.bfloat16
+    M = B * T
+    _require(sq[1] == M, w)
+    a = _scores(q, k.shape[0], B, T, top_k, causal, scale, softcap, slopes, key_begin, key_end, M, w)
+    sk = torch.Size((k.shape[0], M, sq[2]))
+    hq, hk, hv = _heads(q, sq, bf, dev, w), _heads(k, sk, bf, dev, w), _heads(v, sk, bf, dev, w)
+    ho = _heads(out, sq, bf, dev, w)
+    pl = _vector(lse, sq[0] * M, torch.float32, dev, w)
+    ref = ctypes.byref
+    with _On(dev, stream, w) as st:
+        _check(lib.gqe_attention_forward(ref(a), ref(hq), ref(hk), ref(hv), ref(ho), pl, st), w)
+
+
+def gqe_attention_backward(q, k, v, out, lse, dout, dq, dk, dv, B, T, top_k, *, causal=True,
+                           scale=0.0, softcap=0.0, slopes=None, key_begin=None, key_end=None,
+                           workspace=None, stream=None) -> None:
+    """Gradients dq, dk, dv of gqe_attention_forward (same arguments), given its out and lse and
+    the upstream gradient dout (see include/gqe.h)."""
+    w = "gqe_attention_backward"
+    _require(q.dim() == 3 and k.dim() == 3, w)
+    dev, sq, bf = q.device, q.shape, torch.bfloat16
+    M = B * T
+    _require(sq[1] == M, w)
+    a = _scores(q, k.shape[0], B, T, top_k, causal, scale, softcap, slopes, key_begin, key_end, M, w)
+    sk = torch.Size((k.shape[0], M, sq[2]))
+    hq, hk, hv = _heads(q, sq, bf, dev, w), _heads(k, sk, bf, dev, w), _heads(v, sk, bf, dev, w)
+    ho, hd = _heads(out, sq, bf, dev, w), _heads(dout, sq, bf, dev, w)
+    gq, gk, gv = _heads(dq, sq, bf, dev, w), _heads(dk, sk, bf, dev, w), _heads(dv, sk, bf, dev, w)
+    pl = _vector(lse, sq[0] * M, torch.float32, dev, w)
+    ref = ctypes.byref
+    with _On(dev, stream, w) as st:
+        if workspace is None:
+            workspace = _scratch(max(0, lib.gqe_attention_workspace_bytes(ref(a))), dev, stream)
+        _check(lib.gqe_attention_backward(ref(a), ref(hq), ref(hk), ref(hv), ref(ho), pl, ref(hd),
+                                          ref(gq), ref(gk), ref(gv), *_room(workspace, dev, w),
+                                          st), w)
+
+
+def gqe_attention_decode(q, k_cache, v_cache, lengths, out, top_k, *, scale=0.0, softcap=0.0,
+                         slopes=None, key_begin=None, workspace=None, stream=None) -> None:
+    """The single-token form: q [S, B, d_h] at positions `lengths` (int32 [B]; -1: no key) over
+    rows key_begin[b] .. lengths[b] of the caches [G, B, L_max, d_h] (see include/gqe.h)."""
+    w = "gqe_attention_decode"
+    _require(q.dim() == 3 and k_cache.dim() == 4, w)
+    dev, sq, bf = q.device, q.shape, torch.bfloat16
+    G, B, L = k_cache.shape[0], sq[1], k_cache.shape[2]
+    a = _scores(q, G, B, 1, top_k, 1, scale, softcap, slopes, key_begin, None, B, w)
+    sc = torch.Size((G, B, L, sq[2]))
+    hq, ho = _heads(q, sq, bf, dev, w), _heads(out, sq, bf, dev, w)
+    ck, cv = _cache(k_cache, sc, dev, bf, w), _cache(v_cache, sc, dev, bf, w)
+    pos = _vector(lengths, B, torch.int32, dev, w)
+    ref = ctypes.byref
+    with _On(dev, stream, w) as st:
+        if workspace is None:
+            workspace = _scratch(max(0, lib.gqe_attention_decode_workspace_bytes(ref(a), L)), dev,
+                                 stream)
+        _check(lib.gqe_attention_decode(ref(a), ref(hq), ref(ck), ref(cv), L, pos, ref(ho),
+                                        *_room(workspace, dev, w), st), w)
+
+
+def gqe_check_op_status(stream=None, device=None) -> int:
+    """Synchronises the stream and reads and clears the device's status word of the operators
+    above (see include/gqe.h)."""
+    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+    with _On(dev, stream, "gqe_check_op_status") as st:
+        return int(lib.gqe_check_op_status(st))
