@@ -559,6 +559,44 @@ gqe_status gqe_attention_decode(const gqe_scores* a, const gqe_heads* q,
                                 const int32_t* lengths, const gqe_heads* out, void* workspace,
                                 size_t bytes, void* stream);
 
+/* ---------------------------------------------------------------------------------------
+ * The same inside the layer.
+ * ------------------------------------------------------------------------------------- */
+
+/*
+ * gqe_set_qk_transform — norm and rotate the handle's query streams and keys between their
+ * projections and the attention, in gqe_forward, gqe_decode (at positions lengths[b]; the cache
+ * holds the rotated keys) and the backward pass. tr (d_h and dtype as the handle's) is copied;
+ * what it points to is read by every later call. NULL turns it off.
+ *   positions   [B*T] int32, device, read by gqe_forward and the backward pass; NULL: the
+ *               position within the sequence.
+ *   dq_weight,  [d_h] float32, device: gqe_backward (gqe_backward_begin) writes the weights'
+ *   dk_weight   gradients there; a handle restricted to a group range writes its share. NULL:
+ *               not wanted. They may be set anew between a forward and its backward.
+ * gqe_get_tensor's Q and K stay the projections of bf16 handles. Allocates (cudaMalloc) a second
+ * buffer of queries and keys at the first call, and their gradients' where the backward pass
+ * is enabled; not while a stream is being captured.
+ */
+gqe_status gqe_set_qk_transform(gqe_handle h, const gqe_qk_transform* tr,
+                                const int32_t* positions, float* dq_weight, float* dk_weight);
+
+/*
+ * gqe_set_scores — cap, bias and mask the scores of the handle's attention (gqe_scores says how)
+ * in gqe_forward, gqe_decode and the backward pass. scale 0: 1/sqrt(d_h); softcap 0: none.
+ *   slopes      one per stream the handle computes (its group range's routed streams, then the
+ *               shared one), or NULL.
+ *   key_begin,  [B*T] of gqe_forward (with its `causal`), or NULL. gqe_decode reads key_begin as
+ *   key_end     [B], the first visible row of each cache, and no key_end.
+ * All 0 and NULL turns it off. What is pointed to is read by every later call. bf16 handles
+ * only (GQE_ERR_UNSUPPORTED).
+ *
+ * A gqe_backward needs the options of its forward: after a gqe_set_qk_transform or gqe_set_scores
+ * that changed something since (the weights' gradients' addresses aside) it returns
+ * GQE_ERR_INVALID_ARG.
+ */
+gqe_status gqe_set_scores(gqe_handle h, float scale, float softcap, const float* slopes,
+                          const int32_t* key_begin, const int32_t* key_end);
+
 /*
  * gqe_check_op_status — synchronise `stream`, then read and clear the current device's status
  * word of the operators above: GQE_OK, GQE_ERR_TIMEOUT (a wait gave up: outputs since the last

@@ -10,6 +10,7 @@
 #include <new>
 
 #include "gqe_common.cuh"
+#include "layer_options.cuh"
 
 using namespace gqe;
 
@@ -115,7 +116,7 @@ gqe_status gqe_create(gqe_handle* out, int dim, int N, int G, int k, int d_h, gq
   *out = nullptr;
   gqe_status st = check_shape(dim, N, G, k, d_h, dtype, max_tokens);
   if (st != GQE_OK) return st;
-  gqe_ctx* h = new (std::nothrow) gqe_ctx();
+  LayerCtx* h = new (std::nothrow) LayerCtx();
   if (!h) return GQE_ERR_CUDA;
   h->dim = dim;
   h->N = N;
@@ -161,7 +162,8 @@ void gqe_destroy(gqe_handle h) {
   cudaDeviceSynchronize();
   cudaFree(h->ws.base);
   backward_release(h);
-  delete h;
+  layer_options_release(h);
+  delete static_cast<LayerCtx*>(h);
 }
 
 gqe_status gqe_set_group_range(gqe_handle h, int g0, int g1) {
@@ -260,8 +262,10 @@ gqe_status gqe_forward(gqe_handle h, const void* x, int B, int T, const void* W_
             add(fused ? 0 : launch_route_fused(h, M, aux_loss, st)) &&
             add(tc ? launch_tc_qproj(h, x, M, W_q, fused, aux_loss, st)
                    : launch_simt_qproj(h, x, M, W_q, st)) &&
-            add(tc ? launch_tc_attention(h, B, T, S, has_shared, variant, causal, Do, st)
-                   : launch_simt_attention(h, B, T, S, has_shared, variant, causal, Do, st)) &&
+            add(has_options(h)
+                    ? launch_layer_attention(h, B, T, S, has_shared, variant, causal, Do, st)
+                : tc ? launch_tc_attention(h, B, T, S, has_shared, variant, causal, Do, st)
+                     : launch_simt_attention(h, B, T, S, has_shared, variant, causal, Do, st)) &&
             add(launch_combine(h, M, variant, Do, st)) &&
             add(tc ? launch_tc_oproj(h, M, Do, W_o, out, st)
                    : launch_simt_oproj(h, M, Do, W_o, out, st));
@@ -279,6 +283,7 @@ gqe_status gqe_forward(gqe_handle h, const void* x, int B, int T, const void* W_
   h->last_g0 = h->g0;
   h->last_g1 = h->g1;
   h->bwd_begun = 0;
+  options(h).last_forward = options(h).generation;
   return ok ? GQE_OK : GQE_ERR_CUDA;
 }
 
@@ -328,14 +333,18 @@ gqe_status gqe_decode(gqe_handle h, const void* x, int B, void* k_cache, void* v
   // the forward's stages on the B new tokens, with the cache attention in place of the
   // prefill attention
   const bool fused = tc_dense_routes(h);
+  const bool opts = has_options(h);
   int dense = -1;
   bool ok = mark() &&
             add(dense = launch_tc_dense_proj(h, x, M, W_r, W_k, W_v, W_shared, st)) &&
             add(fused ? 0 : launch_route_fused(h, M, aux_loss, st)) &&
             add(launch_tc_qproj(h, x, M, W_q, fused, aux_loss, st)) &&
-            add(launch_tc_decode_attention(h, B, S, has_shared, variant, Do, k_cache, v_cache,
-                                           L_max, lengths, st)) &&
-            add(0) &&  // the combine (gqe slot) runs in the cache attention's finish kernel
+            add(opts ? launch_layer_decode(h, B, S, has_shared, variant, Do, k_cache, v_cache,
+                                           L_max, lengths, st)
+                     : launch_tc_decode_attention(h, B, S, has_shared, variant, Do, k_cache,
+                                                  v_cache, L_max, lengths, st)) &&
+            // without options the combine (gqe slot) runs in the cache attention's finish kernel
+            add(opts ? launch_combine(h, M, variant, Do, st) : 0) &&
             add(launch_tc_oproj(h, M, Do, W_o, out, st));
   if (fused && dense >= 0 && !ok) reset_route_sets(h, st);
   h->last_M = M;

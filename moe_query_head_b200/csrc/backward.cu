@@ -32,6 +32,7 @@
 #include <string.h>
 
 #include "gqe_common.cuh"
+#include "layer_options.cuh"
 
 namespace gqe {
 
@@ -294,7 +295,8 @@ gqe_status check_call(const gqe_ctx* h, const void* x, int B, int T, const void*
   // the saved state must be this layer's last forward, on the same groups
   if (h->last_kind != 1 || h->last_M != c.M || h->last_B != B || h->last_T != T ||
       h->last_variant != variant || h->last_causal != causal ||
-      h->last_shared != c.has_shared || h->last_g0 != h->g0 || h->last_g1 != h->g1)
+      h->last_shared != c.has_shared || h->last_g0 != h->g0 || h->last_g1 != h->g1 ||
+      options(h).last_forward != options(h).generation)
     return GQE_ERR_INVALID_ARG;
   c.Gl = h->g1 - h->g0;
   c.Sr = c.Gl * k;
@@ -357,7 +359,10 @@ gqe_status phase1(gqe_ctx* h, const BwdCall& c, int B, int T, const void* W_o, i
     ++launches;
   }
   if (ok) {
-    const int n = launch_tc_attention_backward(h, b, B, T, c.S, c.has_shared, causal, st);
+    const int n = has_options(h) ? launch_layer_attention_backward(h, b, B, T, c.S, c.has_shared,
+                                                                   causal, st)
+                                 : launch_tc_attention_backward(h, b, B, T, c.S, c.has_shared,
+                                                                causal, st);
     ok = n >= 0;
     launches += n > 0 ? n : 0;
   }
@@ -435,7 +440,7 @@ extern "C" {
 gqe_status gqe_enable_backward(gqe_handle h) {
   if (!h) return GQE_ERR_INVALID_ARG;
   if (!tc_backward_supported(h)) return GQE_ERR_UNSUPPORTED;
-  if (h->bwd_base) return GQE_OK;
+  if (h->bwd_base) return layer_options_alloc(h);
   const size_t bytes = bwd_layout(h->bwd, nullptr, h);
   void* base = nullptr;
   if (cudaMalloc(&base, bytes) != cudaSuccess) {
@@ -460,7 +465,7 @@ gqe_status gqe_enable_backward(gqe_handle h) {
   h->bwd_base = base;
   h->bwd_bytes = bytes;
   h->cublas = hb;
-  return GQE_OK;
+  return layer_options_alloc(h);
 }
 
 gqe_status gqe_backward(gqe_handle h, const void* x, int B, int T, const void* W_r,

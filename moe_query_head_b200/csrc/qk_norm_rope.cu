@@ -156,9 +156,9 @@ __global__ void __launch_bounds__(THREADS) qk_forward_kernel(const __grid_consta
   int pos = 0;
   if (t < A.M) pos = A.positions ? A.positions[t] : (int)(t % A.period);
   if constexpr (APPEND) {
-    // -1: an idle slot; any other position outside the cache is reported. Nothing is written.
+    // -1: an idle slot; other positions outside the cache are reported. Nothing is written.
     if (t < A.M && (pos < 0 || pos >= A.L_max)) {
-      if (pos != -1 && l == 0) atomicExch(A.status, kStatusBadInput);
+      if ((pos != -1 || !A.idle_ok) && l == 0) atomicExch(A.status, kStatusBadInput);
       on = false;
     }
   }

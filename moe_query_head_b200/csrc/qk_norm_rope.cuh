@@ -29,6 +29,7 @@ struct QkArgs {
   float eps = 0.f;
   int L_max = 0;              // append: rows per sequence of the caches
   int32_t* status = nullptr;  // append: device status word
+  int idle_ok = 1;            // append: position -1 marks an idle slot (0: it is reported too)
   // backward
   float* partial = nullptr;  // [kQkPartialRows, d_h] or none (no weight gradient asked for)
   float* dq_weight = nullptr;

@@ -29,7 +29,8 @@ EXPORTED = ("gqe_create", "gqe_forward", "gqe_get_routing", "gqe_get_tensor",
             "gqe_qk_norm_rope", "gqe_qk_norm_rope_workspace_bytes", "gqe_qk_norm_rope_backward",
             "gqe_qk_norm_rope_append", "gqe_attention_forward", "gqe_attention_workspace_bytes",
             "gqe_attention_backward", "gqe_attention_decode_workspace_bytes",
-            "gqe_attention_decode", "gqe_check_op_status")
+            "gqe_attention_decode", "gqe_check_op_status", "gqe_set_qk_transform",
+            "gqe_set_scores")
 GQE_NUM_STAGES = 6
 
 
@@ -133,6 +134,10 @@ def _load() -> ctypes.CDLL:
     lib.gqe_attention_decode_workspace_bytes.restype = I64
     lib.gqe_attention_decode.argtypes = [P, P, P, P, I, P, P, P, SZ, P]
     lib.gqe_attention_decode.restype = I
+    lib.gqe_set_qk_transform.argtypes = [P, P, P, P, P]
+    lib.gqe_set_qk_transform.restype = I
+    lib.gqe_set_scores.argtypes = [P, ctypes.c_float, ctypes.c_float, P, P, P]
+    lib.gqe_set_scores.restype = I
     lib.gqe_check_op_status.argtypes = [P]
     lib.gqe_check_op_status.restype = I
     return lib
@@ -518,6 +523,41 @@ def gqe_attention_decode(q, k_cache, v_cache, lengths, out, top_k, *, scale=0.0,
                                  stream)
         _check(lib.gqe_attention_decode(ref(a), ref(hq), ref(ck), ref(cv), L, pos, ref(ho),
                                         *_room(workspace, dev, w), st), w)
+
+
+def gqe_set_qk_transform(h, d_h=0, dtype=GQE_BF16, *, norm=True, q_weight=None, k_weight=None,
+                         eps=1e-6, inv_freq=None, interleaved=False, positions=None,
+                         dq_weight=None, dk_weight=None) -> None:
+    """Norm and rotation of the handle's queries and keys (see include/gqe.h); d_h = 0 turns
+    them off. The tensors must stay alive while calls of the handle read them."""
+    w = "gqe_set_qk_transform"
+    if not d_h:
+        _check(lib.gqe_set_qk_transform(h, None, None, None, None), w)
+        return
+    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
+
+    def vec(t, n, dt):
+        return None if t is None else _vector(t, n, dt, t.device, w)
+
+    tr = QkTransform(d_h, dtype, int(norm), eps, vec(q_weight, d_h, torch.float32),
+                     vec(k_weight, d_h, torch.float32), rot, int(interleaved),
+                     vec(inv_freq, rot // 2, torch.float64))
+    pos = None if positions is None else vec(positions, positions.numel(), torch.int32)
+    _check(lib.gqe_set_qk_transform(h, ctypes.byref(tr), pos, vec(dq_weight, d_h, torch.float32),
+                                    vec(dk_weight, d_h, torch.float32)), w)
+
+
+def gqe_set_scores(h, *, scale=0.0, softcap=0.0, slopes=None, key_begin=None,
+                   key_end=None) -> None:
+    """Cap, bias and intervals of the handle's scores (see include/gqe.h); without arguments they
+    are off. The tensors must stay alive while calls of the handle read them."""
+    w = "gqe_set_scores"
+
+    def vec(t, dt):
+        return None if t is None else _vector(t, t.numel(), dt, t.device, w)
+
+    _check(lib.gqe_set_scores(h, scale, softcap, vec(slopes, torch.float32),
+                              vec(key_begin, torch.int32), vec(key_end, torch.int32)), w)
 
 
 def gqe_check_op_status(stream=None, device=None) -> int:

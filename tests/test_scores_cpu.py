@@ -236,3 +236,30 @@ def test_norm_rope_form_against_differences(inter):
     # a rotation keeps every pair's length
     y = R.norm_rope(x, w, ang, False, 0.0, 16, inter)
     assert torch.allclose(y.norm(dim=-1), x.norm(dim=-1))
+
+
+def test_layer_options_without_a_handle(G):
+    assert G.lib.gqe_set_qk_transform(None, ctypes.byref(transform(G)), None, None, None) == INV
+    assert G.lib.gqe_set_qk_transform(None, None, None, None, None) == INV
+    assert G.lib.gqe_set_scores(None, 0.0, 1.0, None, None, None) == INV
+
+
+def test_module_options_are_checked():
+    from moe_query_head_b200.module import GQEAttention, document_spans, prefix_spans
+    with pytest.raises(ValueError):
+        GQEAttention(64, 4, 2, head_dim=32, rope_base=1e4, rope_dim=24)
+    with pytest.raises(ValueError):
+        GQEAttention(64, 4, 2, head_dim=32, rope_base=1e4, rope_dim=48)
+    with pytest.raises(ValueError):
+        GQEAttention(64, 4, 2, slopes=[0.1, 0.2])  # three streams
+    with pytest.raises(ValueError):
+        GQEAttention(64, 4, 2, slopes="other")
+    m = GQEAttention(64, 4, 2, qk_norm=True, rope_base=1e4, slopes="geometric")
+    assert {n for n, _ in m.named_parameters()} >= {"q_norm", "k_norm"}
+    with pytest.raises(ValueError):
+        m._ints(torch.zeros(3), 4, "cpu")
+    b, e = document_spans([2, 0, 3], 7)
+    assert b.tolist() == [0, 0, 2, 2, 2, 0, 0] and e.tolist() == [2, 2, 5, 5, 5, 0, 0]
+    with pytest.raises(ValueError):
+        document_spans([5, 3], 7)
+    assert prefix_spans(3, 5).tolist() == [3, 3, 3, 4, 5] and prefix_spans(9, 2).tolist() == [2, 2]
