@@ -67,7 +67,7 @@ struct Cfg {
   static_assert(CTAS * (SMEM + 1024) <= 228 * 1024, "shared memory budget");
 };
 
-// Of every 8 pairs of scores, this many go to the FMA-pipe exponential and the rest to MUFU.
+// Of every 8 pairs of scores, this many take the FMA-pipe exponential and the rest MUFU's.
 constexpr int kFmaPairsOf8 = 3;
 
 struct Params {
@@ -83,8 +83,7 @@ struct Params {
   const float* slopes;
   int T, B, S, Sr, k, nq;
   float scale_log2;  // scale log2(e), of uncapped scores
-  float cap_in;      // scale 2 log2(e) / softcap: the tanh's argument in its exp2 form
-  float cap_log2;    // softcap log2(e), 0: none
+  CapForm cap;
   int32_t* status;
   int64_t spin;
 };
@@ -359,130 +358,143 @@ attn_scores_kernel(const __grid_constant__ Params P) {
     const uint32_t t_s = tmem + lane_off;
     const uint32_t t_p = tmem + lane_off + C::P_COL;
     const uint32_t t_o = tmem + lane_off + C::O_COL;
-    const bool capped = P.cap_log2 != 0.f;
     const float slope2 = P.slopes ? P.slopes[s_idx] * kLog2e : 0.f;
-    const bool biased = P.slopes != nullptr;
-    const float cs = capped || biased ? 1.f : P.scale_log2;
     const int q0 = qt * TQ;
     float m_used = -INFINITY, l = 0.f;
     bool ok = true;
-    for (int j = 0; j < nk; ++j) {
-      if (!warp_wait(s_full, j & 1, P, abort_flag)) { ok = false; break; }
-      tc_fence_after();
-      float s[TK];
-      {
-        uint32_t r[TK];
-        tmem_ld128_wait(t_s, r);
+    by_form(P.cap.on, P.slopes != nullptr, [&](auto cap, auto bias) {
+      constexpr bool CAP = decltype(cap)::value, BIAS = decltype(bias)::value;
+      // a score in log2 units is (tanh of) the product times in, plus the bias
+      const float in = CAP ? P.cap.log2 : P.scale_log2;
+      const float cs = BIAS ? 1.f : in;  // what is still to be multiplied after the registers' pass
+      for (int j = 0; j < nk; ++j) {
+        if (!warp_wait(s_full, j & 1, P, abort_flag)) { ok = false; break; }
+        tc_fence_after();
+        float s[TK];
+        {
+          uint32_t r[TK];
+          tmem_ld128_wait(t_s, r);
 #pragma unroll
-        for (int c = 0; c < TK; ++c) s[c] = __uint_as_float(r[c]);
-      }
-      if (j + 1 < nk) {
+          for (int c = 0; c < TK; ++c) s[c] = __uint_as_float(r[c]);
+        }
+        if (j + 1 < nk) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(s_free);
+        }
+        const int kv0 = (j0 + j) * TK;
+        if constexpr (CAP) {
+          by_flag(!__any_sync(0xffffffffu, !(abs_max<TK>(s) < P.cap.limit)), [&](auto poly) {
+#pragma unroll
+            for (int c = 0; c < TK; c += 2) {
+              const float2 th =
+                  cap_tanh<decltype(poly)::value>(P.cap, make_float2(s[c], s[c + 1]));
+              s[c] = th.x;
+              s[c + 1] = th.y;
+            }
+          });
+        }
+        if constexpr (BIAS) {
+          if (kv0 + TK - 1 <= q0) {
+            // every key at or before every query: the distance is linear (four chains of
+            // additions, eight columns a step: packed constants would have to be moved in)
+            const float base = (float)(kv0 - q) * slope2;
+            const float2 in2 = make_float2(in, in), step = make_float2(8.f * slope2, 8.f * slope2);
+            float2 chain[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              chain[i] = make_float2(fmaf(slope2, (float)(2 * i), base),
+                                     fmaf(slope2, (float)(2 * i + 1), base));
+#pragma unroll
+            for (int c = 0; c < TK; c += 2) {
+              const float2 z = fma2(make_float2(s[c], s[c + 1]), in2, chain[(c >> 1) & 3]);
+              chain[(c >> 1) & 3] = add2(chain[(c >> 1) & 3], step);
+              s[c] = z.x;
+              s[c + 1] = z.y;
+            }
+          } else {
+            const float d0 = (float)(kv0 - q);
+#pragma unroll
+            for (int c = 0; c < TK; ++c) s[c] = fmaf(s[c], in, -slope2 * fabsf(d0 + (float)c));
+          }
+        }
+        if (!whole(j0 + j)) {
+          const int first = b0 - kv0;
+          const uint32_t count = e0 > b0 ? (uint32_t)(e0 - b0) : 0u;
+#pragma unroll
+          for (int c = 0; c < TK; ++c)
+            if ((uint32_t)(c - first) >= count) s[c] = -INFINITY;
+        }
+        // Row maximum in two halves: the exponentials of the first need only its own maximum
+        // and the running reference, so the second half's maximum is formed while they run. A
+        // reference moves only when a maximum passes it by more than the threshold; if the
+        // second half's does, the first half's P is rescaled.
+        const float m_old = m_used;
+        uint32_t pk[TK / 2];
+        float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        auto half = [&](auto hc) {
+          constexpr int H = decltype(hc)::value, C0 = 64 * H;
+          const float m = max64(s + C0) * cs;
+          if (m > m_used + kRescaleThreshold) {
+            if constexpr (H == 1) {
+              // a first half without keys holds only zeros (2^-125): the factor is then 0
+              const float a2 = ex2(m_used - m);
+#pragma unroll
+              for (int x = 0; x < TK / 4; ++x)
+                pk[x] = pack_bf16x2(__uint_as_float(pk[x] << 16) * a2,
+                                    __uint_as_float(pk[x] & 0xffff0000u) * a2);
+              if constexpr (!C::SUM_MMA) {
+                ls[0] = mul2(ls[0], make_float2(a2, a2));
+                ls[1] = mul2(ls[1], make_float2(a2, a2));
+              }
+            }
+            m_used = m;
+          }
+          const float ref = m_used == -INFINITY ? 0.f : m_used;
+          const float2 cs2 = make_float2(cs, cs), nm2 = make_float2(-ref, -ref);
+#pragma unroll
+          for (int x = 0; x < 32; ++x) {
+            const float2 v = make_float2(s[C0 + 2 * x], s[C0 + 2 * x + 1]);
+            const float2 t = BIAS ? add2(v, nm2) : fma2(v, cs2, nm2);
+            const float2 p = (x & 7) >= 8 - kFmaPairsOf8 ? exp2_fma2_nan(t)
+                                                         : make_float2(ex2(t.x), ex2(t.y));
+            if constexpr (!C::SUM_MMA) ls[x & 1] = add2(ls[x & 1], p);
+            pk[32 * H + x] = pack_bf16x2(p.x, p.y);
+          }
+        };
+        half(std::integral_constant<int, 0>{});
+        half(std::integral_constant<int, 1>{});
+        const bool need = j > 0 && m_used != m_old;
+        const float alpha = need ? ex2(m_old - m_used) : 1.f;  // 0 from a reference of -inf
+        if constexpr (!C::SUM_MMA) {
+          const float2 a = add2(ls[0], ls[1]);
+          l = l * alpha + (a.x + a.y);
+        }
+        if (j > 0 && !warp_wait(pv_done, (j - 1) & 1, P, abort_flag)) { ok = false; break; }
+        if (__any_sync(0xffffffffu, need)) {
+          tc_fence_after();
+#pragma unroll
+          for (int c0 = 0; c0 < C::N_PV; c0 += 16) {
+            uint32_t r[16];
+            tmem_ld16_wait(t_o + c0, r);
+#pragma unroll
+            for (int x = 0; x < 16; ++x) r[x] = __float_as_uint(__uint_as_float(r[x]) * alpha);
+            tmem_st16(t_o + c0, r);
+          }
+        }
+#pragma unroll
+        for (int c0 = 0; c0 < TK / 2; c0 += 16) {
+          uint32_t r[16];
+#pragma unroll
+          for (int x = 0; x < 16; ++x) r[x] = pk[c0 + x];
+          tmem_st16(t_p + c0, r);
+        }
+        tmem_wait_st();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(s_free);
+        if (lane == 0) mbar_arrive(p_ready);
       }
-      const int kv0 = (j0 + j) * TK;
-      // cap and bias, leaving the scores in log2 units
-      if (capped) {
-#pragma unroll
-        for (int c = 0; c < TK; ++c) s[c] = tanh_from_2log2(s[c] * P.cap_in) * P.cap_log2;
-      }
-      if (biased) {
-        const float in = capped ? 1.f : P.scale_log2;
-        const float d0 = (float)(kv0 - q);
-        if (kv0 + TK - 1 <= q0) {
-          // every key at or before every query: the distance is linear
-          const float base = d0 * slope2;
-#pragma unroll
-          for (int c = 0; c < TK; ++c) s[c] = fmaf(s[c], in, fmaf(slope2, (float)c, base));
-        } else {
-#pragma unroll
-          for (int c = 0; c < TK; ++c) s[c] = fmaf(s[c], in, -slope2 * fabsf(d0 + (float)c));
-        }
-      }
-      if (!whole(j0 + j)) {
-        const int first = b0 - kv0, last = e0 - kv0;
-#pragma unroll
-        for (int c = 0; c < TK; ++c)
-          if (c < first || c >= last) s[c] = -INFINITY;
-      }
-      // Row maximum in two halves: the exponentials of the first need only its own maximum
-      // and the running reference, so the second half's maximum is formed while they run.
-      const float m_old = m_used;
-      const float m_a = max64(s) * cs;
-      if (m_a > m_used + kRescaleThreshold) m_used = m_a;
-      const float2 cs2 = make_float2(cs, cs);
-      uint32_t pk[TK / 2];
-      float2 lsa[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-      float2 lsb[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-      {
-        const float ref = m_used == -INFINITY ? 0.f : m_used;
-        const float2 nm2 = make_float2(-ref, -ref);
-#pragma unroll
-        for (int x = 0; x < TK / 4; ++x) {
-          const float2 t = fma2(make_float2(s[2 * x], s[2 * x + 1]), cs2, nm2);
-          const float2 p = (x & 7) >= 8 - kFmaPairsOf8 ? exp2_fma2_nan(t)
-                                                       : make_float2(ex2(t.x), ex2(t.y));
-          if constexpr (!C::SUM_MMA) lsa[x & 1] = add2(lsa[x & 1], p);
-          pk[x] = pack_bf16x2(p.x, p.y);
-        }
-      }
-      const float m_b = max64(s + 64) * cs;
-      if (m_b > m_used + kRescaleThreshold) {
-        // a first half without keys holds only zeros (2^-125): the factor is then 0
-        const float a2 = ex2(m_used - m_b);
-#pragma unroll
-        for (int x = 0; x < TK / 4; ++x)
-          pk[x] = pack_bf16x2(__uint_as_float(pk[x] << 16) * a2,
-                              __uint_as_float(pk[x] & 0xffff0000u) * a2);
-        if constexpr (!C::SUM_MMA) {
-          lsa[0] = mul2(lsa[0], make_float2(a2, a2));
-          lsa[1] = mul2(lsa[1], make_float2(a2, a2));
-        }
-        m_used = m_b;
-      }
-      {
-        const float ref = m_used == -INFINITY ? 0.f : m_used;
-        const float2 nm2 = make_float2(-ref, -ref);
-#pragma unroll
-        for (int x = TK / 4; x < TK / 2; ++x) {
-          const float2 t = fma2(make_float2(s[2 * x], s[2 * x + 1]), cs2, nm2);
-          const float2 p = (x & 7) >= 8 - kFmaPairsOf8 ? exp2_fma2_nan(t)
-                                                       : make_float2(ex2(t.x), ex2(t.y));
-          if constexpr (!C::SUM_MMA) lsb[x & 1] = add2(lsb[x & 1], p);
-          pk[x] = pack_bf16x2(p.x, p.y);
-        }
-      }
-      const bool need = j > 0 && m_used != m_old;
-      const float alpha = need ? ex2(m_old - m_used) : 1.f;  // 0 from a reference of -inf
-      if constexpr (!C::SUM_MMA) {
-        const float2 a = add2(add2(lsa[0], lsa[1]), add2(lsb[0], lsb[1]));
-        l = l * alpha + (a.x + a.y);
-      }
-      if (j > 0 && !warp_wait(pv_done, (j - 1) & 1, P, abort_flag)) { ok = false; break; }
-      if (__any_sync(0xffffffffu, need)) {
-        tc_fence_after();
-#pragma unroll
-        for (int c0 = 0; c0 < C::N_PV; c0 += 16) {
-          uint32_t r[16];
-          tmem_ld16_wait(t_o + c0, r);
-#pragma unroll
-          for (int x = 0; x < 16; ++x) r[x] = __float_as_uint(__uint_as_float(r[x]) * alpha);
-          tmem_st16(t_o + c0, r);
-        }
-      }
-#pragma unroll
-      for (int c0 = 0; c0 < TK / 2; c0 += 16) {
-        uint32_t r[16];
-#pragma unroll
-        for (int x = 0; x < 16; ++x) r[x] = pk[c0 + x];
-        tmem_st16(t_p + c0, r);
-      }
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(p_ready);
-    }
+    });
     // ---- epilogue: O / l into the output row
     if (ok && nk > 0) ok = warp_wait(o_full, 0, P, abort_flag);
     if (ok) {
@@ -590,8 +602,7 @@ int launch_dh(const AttnArgs& a, cudaStream_t st) {
   P.k = a.k;
   P.nq = (a.T + TQ - 1) / TQ;
   P.scale_log2 = a.scale * kLog2e;
-  P.cap_in = a.softcap > 0.f ? 2.f * a.scale * kLog2e / a.softcap : 0.f;
-  P.cap_log2 = a.softcap * kLog2e;
+  P.cap = cap_form(a.scale, a.softcap);
   P.status = a.status;
   P.spin = a.spin > 0 ? a.spin : (int64_t)1 << 22;
   const int64_t items = (int64_t)a.B * a.S * P.nq;

@@ -9,6 +9,8 @@
 
 #include <cuda.h>
 
+#include <type_traits>
+
 #include "gqe_common.cuh"
 #include "qk_norm_rope.cuh"
 #include "tc_ptx.cuh"
@@ -85,6 +87,81 @@ __device__ __forceinline__ float tanh_from_2log2(float x2) {
   return fmaf(-2.f, rcp_approx(ex2(x2) + 1.f), 1.f);
 }
 
+// The cap's tanh of a pair of scores. An odd polynomial of degree 9 on the FMA pipe serves
+// scores whose tanh argument lies in [-1, 1] (the ordinary case: caps are chosen above the
+// scores); others take the exponential and a reciprocal, 16 cycles of the MUFU unit per score
+// and warp against the polynomial's 6 of the FMA pipe. x Q(x^2) was fitted for minimal largest
+// relative error on [0, 1] (iteratively reweighted least squares): 7e-6 in float32, which
+// moves a weight by less than a tenth of its bf16 step at a cap of 50. The host folds the
+// scores' factor into the coefficients, so the raw score is the polynomial's argument.
+struct CapForm {
+  float2 c[5];   // Q's coefficients times factor^(2 i + 1), each twice
+  float limit;   // largest |score| the polynomial serves
+  float t2;      // factor 2 log2(e): the argument of tanh_from_2log2
+  float log2;    // softcap log2(e)
+  int on;
+};
+inline CapForm cap_form(float scale, float softcap) {
+  CapForm f = {};
+  if (!(softcap > 0.f)) return f;
+  const double q[5] = {0.9999930893856743, -0.33298065253491427, 0.13036811257418396,
+                       -0.04481755463875348, 0.009036424252608788};
+  const double x = (double)scale / softcap;
+  double power = x;
+  for (int i = 0; i < 5; ++i) {
+    f.c[i] = make_float2((float)(q[i] * power), (float)(q[i] * power));
+    power *= x * x;
+  }
+  f.limit = (float)(1.0 / x);
+  f.t2 = (float)(x * 2.8853900817779268);
+  f.log2 = softcap * 1.4426950408889634f;
+  f.on = 1;
+  // beyond float32's range for the coefficients nothing is served by the polynomial
+  if (!(f.limit < 1e4f && f.limit > 1e-4f)) f.limit = 0.f;
+  return f;
+}
+template <bool POLY>
+__device__ __forceinline__ float2 cap_tanh(const CapForm& f, float2 s) {
+  if constexpr (POLY) {
+    const float2 y = mul2(s, s);
+    float2 p = fma2(f.c[4], y, f.c[3]);
+    p = fma2(p, y, f.c[2]);
+    p = fma2(p, y, f.c[1]);
+    p = fma2(p, y, f.c[0]);
+    return mul2(p, s);
+  } else {
+    return make_float2(tanh_from_2log2(s.x * f.t2), tanh_from_2log2(s.y * f.t2));
+  }
+}
+// Largest |s| of N scores (NaN aside).
+template <int N>
+__device__ __forceinline__ float abs_max(const float* s) {
+  float m[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < N; i += 2) m[(i >> 1) & 3] = fmax3(m[(i >> 1) & 3], fabsf(s[i]), fabsf(s[i + 1]));
+  return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+
+// Runs f with the compile-time flags of the score's form (the same for the whole grid).
+template <typename F>
+__device__ __forceinline__ void by_form(bool cap, bool bias, F&& f) {
+  using Yes = std::integral_constant<bool, true>;
+  using No = std::integral_constant<bool, false>;
+  if (cap) {
+    if (bias) f(Yes{}, Yes{});
+    else f(Yes{}, No{});
+  } else {
+    if (bias) f(No{}, Yes{});
+    else f(No{}, No{});
+  }
+}
+// Runs f with a warp-uniform flag as a compile-time one.
+template <typename F>
+__device__ __forceinline__ void by_flag(bool flag, F&& f) {
+  if (flag) f(std::integral_constant<bool, true>{});
+  else f(std::integral_constant<bool, false>{});
+}
+
 // 2^x of a pair on the FMA pipe, as exp2_fma.cuh's exp2_fma2 (nearest integer n of x by adding
 // and subtracting 1.5 * 2^23, then the degree-2 polynomial of 2^(x - n) fitted there, 1.9e-3,
 // the size of the bf16 rounding that follows), with NaN kept: the clamp passes a NaN on and
@@ -126,27 +203,35 @@ __device__ __forceinline__ void span_of(const SpanArgs& P, int b, int q, int& b0
 // Sets every infinity and NaN of a tile of bf16 values in shared memory to zero; true if there
 // was one. Warp-collective. A masked weight is zero, and zero times a NaN would reach the row
 // through the tensor cores, so tiles that some row sees only in part are cleaned first.
+// The first pass multiplies every value by zero and adds it up (a NaN says that one was not
+// finite); only then the second looks for them.
 __device__ __forceinline__ bool clean_tile(uint8_t* tile, int bytes) {
-  bool bad = false;
   const int lane = threadIdx.x & 31;
+  const __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f);
+  __nv_bfloat162 acc[4] = {zero, zero, zero, zero};
 #pragma unroll 4
   for (int i = lane * 16; i < bytes; i += 512) {
-    uint4 v = *reinterpret_cast<const uint4*>(tile + i);
-    // exponent field all ones: adding one unit of it carries into (or past) the sign bit
-    const uint32_t c = ((v.x & 0x7f807f80u) + 0x00800080u) | ((v.y & 0x7f807f80u) + 0x00800080u) |
-                       ((v.z & 0x7f807f80u) + 0x00800080u) | ((v.w & 0x7f807f80u) + 0x00800080u);
-    if (c & 0x80008000u) {
-      bad = true;
-      uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    const uint4 v = *reinterpret_cast<const uint4*>(tile + i);
+    acc[0] = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&v.x), zero, acc[0]);
+    acc[1] = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&v.y), zero, acc[1]);
+    acc[2] = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&v.z), zero, acc[2]);
+    acc[3] = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&v.w), zero, acc[3]);
+  }
+  const __nv_bfloat162 all = __hadd2(__hadd2(acc[0], acc[1]), __hadd2(acc[2], acc[3]));
+  if (!__any_sync(0xffffffffu, (*reinterpret_cast<const uint32_t*>(&all) & 0x7fff7fffu) != 0u))
+    return false;
+#pragma unroll 1
+  for (int i = lane * 16; i < bytes; i += 512) {
+    uint32_t* w = reinterpret_cast<uint32_t*>(tile + i);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        if ((w[e] & 0x00007f80u) == 0x00007f80u) w[e] &= 0xffff0000u;
-        if ((w[e] & 0x7f800000u) == 0x7f800000u) w[e] &= 0x0000ffffu;
-      }
-      *reinterpret_cast<uint4*>(tile + i) = make_uint4(w[0], w[1], w[2], w[3]);
+    for (int e = 0; e < 4; ++e) {
+      uint32_t x = w[e];
+      if ((x & 0x00007f80u) == 0x00007f80u) x &= 0xffff0000u;
+      if ((x & 0x7f800000u) == 0x7f800000u) x &= 0x0000ffffu;
+      w[e] = x;
     }
   }
-  return __any_sync(0xffffffffu, bad);
+  return true;
 }
 
 }  // namespace gqe

@@ -34,7 +34,7 @@ using namespace tc;
 
 constexpr int THREADS = 256;
 constexpr int TQ = 128, TK = 128;
-constexpr int kSmallRegs = 48, kLargeRegs = 208;  // as the forward's register split
+constexpr int kSmallRegs = 64, kLargeRegs = 192;  // of the two warpgroups, by setmaxnreg
 static_assert(kSmallRegs * 128 + kLargeRegs * 128 == THREADS * (65536 / (2 * THREADS)),
               "register split must equal the launch allocation");
 
@@ -66,7 +66,9 @@ struct Params {
   int64_t sel_stride;
   int sel_off, experts;
   int T, B, S, Sr, k, G, nq;
-  float scale, scale_log2, cap_in, cap_log2;
+  int split;  // CTAs (a cluster) that share the jobs of a key tile
+  float scale, scale_log2;
+  CapForm cap;
   int32_t* status;
   int64_t spin;
 };
@@ -128,36 +130,10 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
       : "memory");
 }
 
-// A score of the products in log2 units (capped, biased) and the cap's derivative factor.
+// Of every 8 pairs of scores, this many take the FMA-pipe exponential and the rest MUFU's: none
+// where the cap's polynomial keeps the FMA pipe busy.
 template <bool CAP, bool BIAS>
-__device__ __forceinline__ float score(const Params& P, float s, float slope2, float dist,
-                                       float& dcap) {
-  float z;
-  if constexpr (CAP) {
-    const float th = tanh_from_2log2(s * P.cap_in);
-    dcap = fmaf(-th, th, 1.f);
-    z = th * P.cap_log2;
-  } else {
-    dcap = 1.f;
-    z = s * P.scale_log2;
-  }
-  if constexpr (BIAS) z = fmaf(-slope2, fabsf(dist), z);
-  return z;
-}
-
-// Runs f with the compile-time flags of the score's form (the same for the whole grid).
-template <typename F>
-__device__ __forceinline__ void by_form(bool cap, bool bias, F&& f) {
-  using Yes = std::integral_constant<bool, true>;
-  using No = std::integral_constant<bool, false>;
-  if (cap) {
-    if (bias) f(Yes{}, Yes{});
-    else f(Yes{}, No{});
-  } else {
-    if (bias) f(No{}, Yes{});
-    else f(No{}, No{});
-  }
-}
+constexpr int kBwdFma = CAP ? 0 : 2;
 
 // Writes a TMEM accumulator row (DH columns, scaled) as bf16.
 template <int DH>
@@ -461,8 +437,9 @@ attn_scores_dq_kernel(const __grid_constant__ Params P) {
     const float lse = live ? P.lse[srow] : 0.f;
     const float dsum = live ? P.dsum[srow] : 0.f;
     const float slope2 = P.slopes ? P.slopes[s_idx] * kLog2e : 0.f;
+    const int q0 = qt * TQ;
     bool ok = true;
-    by_form(P.cap_log2 != 0.f, P.slopes != nullptr, [&](auto cap, auto bias) {
+    by_form(P.cap.on, P.slopes != nullptr, [&](auto cap, auto bias) {
       constexpr bool CAP = decltype(cap)::value, BIAS = decltype(bias)::value;
       for (int j = 0; j < nk; ++j) {
         if (!warp_wait(sdp_full, j & 1, P)) { ok = false; break; }
@@ -470,34 +447,79 @@ attn_scores_dq_kernel(const __grid_constant__ Params P) {
         const int kv0 = (j0 + j) * Q::TKD;
         uint32_t pk[32];
         {
-          uint32_t sr[64], dr[64];
-          tmem_ld64_wait(t_base + Q::S_COL, sr);
+          float sr[64];
+          uint32_t dr[64];
+          {
+            uint32_t r[64];
+            tmem_ld64_wait(t_base + Q::S_COL, r);
+#pragma unroll
+            for (int c = 0; c < 64; ++c) sr[c] = __uint_as_float(r[c]);
+          }
           tmem_ld64_wait(t_base + Q::DP_COL, dr);
           if (j + 1 < nk) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(s_free);
           }
-          const float d0 = (float)(kv0 - q);
-          auto one = [&](int c) {
-            float dc;
-            const float z =
-                score<CAP, BIAS>(P, __uint_as_float(sr[c]), slope2, d0 + (float)c, dc);
-            const float v = ex2(z - lse) * (__uint_as_float(dr[c]) - dsum);
-            return CAP ? v * dc : v;
+          const bool poly = !CAP || !__any_sync(0xffffffffu, !(abs_max<64>(sr) < P.cap.limit));
+          const float in = CAP ? P.cap.log2 : P.scale_log2;
+          const float2 in2 = make_float2(in, in), nl2 = make_float2(-lse, -lse);
+          const float2 nD2 = make_float2(-dsum, -dsum);
+          // dz of the scores' columns 2x, 2x + 1, their bias and -lse in b
+          auto pair = [&](int x, float2 b, auto pl) {
+            float2 v = make_float2(sr[2 * x], sr[2 * x + 1]);
+            if constexpr (CAP) v = cap_tanh<decltype(pl)::value>(P.cap, v);
+            const float2 t = fma2(v, in2, b);
+            const float2 p = (x & 7) >= 8 - kBwdFma<CAP, BIAS>
+                                 ? exp2_fma2_nan(t)
+                                 : make_float2(ex2(t.x), ex2(t.y));
+            float2 d = mul2(p, add2(make_float2(__uint_as_float(dr[2 * x]),
+                                                __uint_as_float(dr[2 * x + 1])), nD2));
+            if constexpr (CAP)
+              d = mul2(d, fma2(mul2(v, v), make_float2(-1.f, -1.f), make_float2(1.f, 1.f)));
+            return d;
           };
-          if (whole(j0 + j)) {
+          const float d0 = (float)(kv0 - q);
+          auto all = [&](auto pl) {
+          if (!BIAS || kv0 + Q::TKD - 1 <= q0) {
+            // no bias, or every key at or before every query: the distance is linear (four
+            // chains of additions, eight columns a step: packed constants would be moved in)
+            const float base = fmaf(d0, slope2, -lse);
+            const float2 step = make_float2(8.f * slope2, 8.f * slope2);
+            float2 chain[4];
 #pragma unroll
-            for (int x = 0; x < 32; ++x) pk[x] = pack_bf16x2(one(2 * x), one(2 * x + 1));
-          } else {
-            const int first = b0 - kv0, last = e0 - kv0;
+            for (int i = 0; i < 4; ++i)
+              chain[i] = make_float2(fmaf(slope2, (float)(2 * i), base),
+                                     fmaf(slope2, (float)(2 * i + 1), base));
 #pragma unroll
             for (int x = 0; x < 32; ++x) {
-              const float v0 = one(2 * x), v1 = one(2 * x + 1);
-              pk[x] = pack_bf16x2(2 * x >= first && 2 * x < last ? v0 : 0.f,
-                                  2 * x + 1 >= first && 2 * x + 1 < last ? v1 : 0.f);
+              const float2 d = pair(x, BIAS ? chain[x & 3] : nl2, pl);
+              if constexpr (BIAS) chain[x & 3] = add2(chain[x & 3], step);
+              sr[2 * x] = d.x;
+              sr[2 * x + 1] = d.y;
+            }
+          } else {
+#pragma unroll
+            for (int x = 0; x < 32; ++x) {
+              const float2 d =
+                  pair(x, make_float2(fmaf(-slope2, fabsf(d0 + (float)(2 * x)), -lse),
+                                      fmaf(-slope2, fabsf(d0 + (float)(2 * x + 1)), -lse)), pl);
+              sr[2 * x] = d.x;
+              sr[2 * x + 1] = d.y;
             }
           }
+          };
+          if (CAP && !poly) all(std::integral_constant<bool, false>{});
+          else all(std::integral_constant<bool, true>{});
+          if (!whole(j0 + j)) {
+            const int first = b0 - kv0;
+            const uint32_t count = live ? (uint32_t)(e0 - b0) : 0u;
+#pragma unroll
+            for (int c = 0; c < 64; ++c)
+              if ((uint32_t)(c - first) >= count) sr[c] = 0.f;
+          }
+#pragma unroll
+          for (int x = 0; x < 32; ++x) pk[x] = pack_bf16x2(sr[2 * x], sr[2 * x + 1]);
         }
         // the previous dQ product has read dz: it may be overwritten
         if (j > 0 && !warp_wait(d_free, (j - 1) & 1, P)) { ok = false; break; }
@@ -540,19 +562,51 @@ attn_scores_dq_kernel(const __grid_constant__ Params P) {
 // columns of their own: at two CTAs per SM (256 columns) 48 queries for head dims up to 48
 // and 32 for 64; at one CTA per SM (512 columns) 64.
 // ---------------------------------------------------------------------------------------
+constexpr int kMaxSplit = 4;  // CTAs of a cluster that share an item's jobs
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// The address of a shared-memory location of this CTA in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t map_shared(uint32_t addr, int rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void st_cluster_v4(uint32_t addr, const uint32_t* v) {
+  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3])
+               : "memory");
+}
+__device__ __forceinline__ void tmem_ld8_wait(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7])
+      : "r"(taddr)
+      : "memory");
+}
+
 template <int DH>
 struct KCfg {
   using C = BCfg<DH>;
   static constexpr int TQJ = DH <= 48 ? 48 : (DH <= 64 ? 32 : 64);
   static constexpr int QT_BYTES = TQJ * DH * 2;
   static constexpr int STAGES = C::STAGES;
-  // per softmax warp: two buffers of a job's lse, D, first keys and ends of keys
-  static constexpr int WARP_STAGE = 4 * 2 * 4 * TQJ * 4;
-  static constexpr int SMEM = 2 * C::TILE_BYTES + STAGES * 2 * QT_BYTES + 1024 + 512 + WARP_STAGE;
+  // per stage a job's -lse, -D, first keys, ends of keys, and whether it is seen whole
+  static constexpr int STAT_BYTES = (4 * TQJ + 4) * 4;
+  static constexpr int SMEM =
+      2 * C::TILE_BYTES + STAGES * (2 * QT_BYTES + STAT_BYTES) + 1024 + 512;
   static constexpr int S_COL = 0, DP_COL = TQJ, P_COL = 2 * TQJ, DS_COL = 2 * TQJ + TQJ / 2;
   static constexpr int DV_COL = 3 * TQJ, DK_COL = 3 * TQJ + DH;
   static_assert(TQJ % 16 == 0 && TQJ <= 64, "a job's queries: two per lane at most");
   static_assert(DK_COL + DH <= C::TMEM_COLS, "TMEM budget");
+  static_assert(DK_COL == DV_COL + DH, "the cluster's sum takes [dV | dK] as one row");
+  static_assert((kMaxSplit - 1) * 128 * (2 * DH / kMaxSplit) * 4 <=
+                    2 * C::TILE_BYTES + STAGES * 2 * QT_BYTES,
+                "the tiles' memory holds the other CTAs' parts");
+  static_assert(2 * DH / kMaxSplit % 8 == 0, "parts of whole 16-byte stores");
   static_assert(C::CTAS * (SMEM + 1024) <= 228 * 1024, "shared memory per SM");
 };
 
@@ -569,8 +623,8 @@ attn_scores_dkdv_kernel(const __grid_constant__ Params P) {
   uint8_t* sV = sK + C::TILE_BYTES;
   uint8_t* sQ = sV + C::TILE_BYTES;
   uint8_t* sdO = sQ + K::STAGES * K::QT_BYTES;
-  float* wstage = reinterpret_cast<float*>(sdO + K::STAGES * K::QT_BYTES);
-  uint64_t* bar = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(wstage) + K::WARP_STAGE);
+  uint8_t* sStat = sdO + K::STAGES * K::QT_BYTES;
+  uint64_t* bar = reinterpret_cast<uint64_t*>(sStat + K::STAGES * K::STAT_BYTES);
   uint64_t* kv_full = bar;
   uint64_t* r_full = bar + 1;
   uint64_t* r_empty = r_full + K::STAGES;
@@ -585,7 +639,8 @@ attn_scores_dkdv_kernel(const __grid_constant__ Params P) {
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   // first key tiles first: under a causal mask the most queries see them
   const int bg = P.B * P.G;
-  const int kt = blockIdx.x / bg, g = blockIdx.x % bg % P.G, b_idx = blockIdx.x % bg / P.G;
+  const int item = blockIdx.x / P.split, part = blockIdx.x % P.split;  // part: rank in the cluster
+  const int kt = item / bg, g = item % bg % P.G, b_idx = item % bg / P.G;
   const int u0 = kt * TK, u1 = min(u0 + TK, P.T);
   if (threadIdx.x == 0) {
     mbar_init(kv_full, 1);
@@ -647,24 +702,12 @@ attn_scores_dkdv_kernel(const __grid_constant__ Params P) {
   const int qt0 = q_lo / TQJ;
   const int per = q_lo < q_hi ? (q_hi + TQJ - 1) / TQJ - qt0 : 0;  // query tiles of a stream
   const int ns = P.k + (g == 0 && P.S > P.Sr ? 1 : 0);             // streams of the head
-  const int nj = ns * per;
+  // this CTA's share of the item's jobs: nj from job (si0, r0) on
+  const int nj_all = ns * per;
+  const int j_first = (int)((int64_t)nj_all * part / P.split);
+  const int nj = (int)((int64_t)nj_all * (part + 1) / P.split) - j_first;
+  const int si0 = per > 0 ? j_first / per : 0, r0 = per > 0 ? j_first % per : 0;
   auto stream_of = [&](int si) { return si < P.k ? g * P.k + si : P.Sr; };
-  // Whether every query of a job sees every key of the tile; lane l holds the intervals of
-  // queries l and l + 32 of the job.
-  auto job_spans = [&](int qt, int (&jb)[2], int (&je)[2]) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      jb[h] = 0;
-      je[h] = 0;
-      if (lane + 32 * h < TQJ) span_of(P.span, b_idx, qt * TQJ + lane + 32 * h, jb[h], je[h]);
-    }
-  };
-  auto whole = [&](const int (&jb)[2], const int (&je)[2]) {
-    bool w = jb[0] <= u0 && je[0] >= u1;
-    if (lane + 32 < TQJ) w = w && jb[1] <= u0 && je[1] >= u1;
-    return __all_sync(0xffffffffu, w) != 0;
-  };
-
   if (warp < 4) {
     if constexpr (C::CTAS == 2) setmaxnreg_dec<kSmallRegs>();
     if (warp == 0) {
@@ -673,7 +716,7 @@ attn_scores_dkdv_kernel(const __grid_constant__ Params P) {
         mbar_arrive_expect_tx(kv_full, 2 * C::TILE_BYTES);
         tma_load_5d(sK, &P.tm_k, 0, u0, 0, g, b_idx, kv_full);
         tma_load_5d(sV, &P.tm_v, 0, u0, 0, g, b_idx, kv_full);
-        int st = 0, si = 0, r = 0;
+        int st = 0, si = si0, r = r0;
         uint32_t ph = 0;
         for (int j = 0; j < nj; ++j) {
           if (!lane_wait(&r_empty[st], ph ^ 1, P)) break;
@@ -692,23 +735,62 @@ attn_scores_dkdv_kernel(const __grid_constant__ Params P) {
         }
       }
     } else if (warp == 3) {
-      // ------------------------------------------ cleaning of the q and dout tiles of jobs
-      // that are seen in part; passes every job on to the MMA warp
-      int st = 0, r = 0;
+      // ------------------------------------------ per job: the rows' lse, D and intervals
+      // for the softmax warps, and the cleaning of q and dout tiles that are seen in part
+      int st = 0, si = si0, r = r0;
       uint32_t ph = 0;
+      // lane l holds queries l and l + 32 of a job, loaded a job ahead
       int jb[2], je[2];
-      job_spans(qt0, jb, je);
+      float nl[2], nd[2];
+      auto fetch = [&]() {
+        const int64_t base = (int64_t)stream_of(si) * P.B * P.T + (int64_t)b_idx * P.T;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int qq = (qt0 + r) * TQJ + lane + 32 * h;
+          jb[h] = je[h] = 0;
+          nl[h] = nd[h] = 0.f;
+          if (lane + 32 * h < TQJ) {
+            span_of(P.span, b_idx, qq, jb[h], je[h]);
+            if (qq < P.T) {
+              nl[h] = -P.lse[base + qq];
+              nd[h] = -P.dsum[base + qq];
+            }
+          }
+        }
+        if (++r == per) {
+          r = 0;
+          ++si;
+        }
+      };
+      if (nj > 0) fetch();
       for (int j = 0; j < nj; ++j) {
-        const bool w = whole(jb, je);
-        if (++r == per) r = 0;
-        if (j + 1 < nj) job_spans(qt0 + r, jb, je);
+        // the stage's statistics were read before its products ended
+        if (!warp_wait(&r_empty[st], ph ^ 1, P)) break;
+        float* f = reinterpret_cast<float*>(sStat + st * K::STAT_BYTES);
+        int* fi = reinterpret_cast<int*>(f + 2 * TQJ);
+        bool w = true;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int c = lane + 32 * h;
+          if (c < TQJ) {
+            const bool live = jb[h] < je[h];  // false for queries past the sequence
+            f[c] = live ? nl[h] : 0.f;
+            f[TQJ + c] = live ? nd[h] : 0.f;
+            fi[c] = jb[h];
+            fi[TQJ + c] = je[h];
+            w = w && jb[h] <= u0 && je[h] >= u1;
+          }
+        }
+        w = __all_sync(0xffffffffu, w) != 0;
+        if (lane == 0) fi[2 * TQJ] = w;
+        if (j + 1 < nj) fetch();
         if (!warp_wait(&r_full[st], ph, P)) break;
         if (!w) {
           const bool bq = clean_tile(sQ + st * K::QT_BYTES, K::QT_BYTES);
           const bool bd = clean_tile(sdO + st * K::QT_BYTES, K::QT_BYTES);
           if (bq || bd) fence_async_shared();
-          __syncwarp();
         }
+        __syncwarp();
         if (lane == 0) mbar_arrive(&r_clean[st]);
         if (++st == K::STAGES) {
           st = 0;
@@ -790,105 +872,112 @@ attn_scores_dkdv_kernel(const __grid_constant__ Params P) {
     const int row = (warp & 3) * 32 + lane;  // key row of the tile
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t t_base = tmem + lane_off;
-    float* wL = wstage + (warp & 3) * (2 * 4 * TQJ);  // [2][4][TQJ]: lse, D, first, end
     const int u = u0 + row;
     const bool key_ok = u < P.T;
     bool ok = true;
-    // a job's lse, D and intervals: lane l loads queries l and l + 32, one job ahead
-    float nl[2], nd[2];
-    int jb[2], je[2];
-    auto fetch = [&](int si, int qt) {
-      job_spans(qt, jb, je);
-      const int64_t base = (int64_t)stream_of(si) * P.B * P.T + (int64_t)b_idx * P.T;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const bool live = jb[h] < je[h];  // false for queries past the sequence
-        nl[h] = live ? P.lse[base + qt * TQJ + lane + 32 * h] : 0.f;
-        nd[h] = live ? P.dsum[base + qt * TQJ + lane + 32 * h] : 0.f;
-      }
-    };
-    if (nj > 0) fetch(0, qt0);
-    by_form(P.cap_log2 != 0.f, P.slopes != nullptr, [&](auto cap, auto bias) {
+    by_form(P.cap.on, P.slopes != nullptr, [&](auto cap, auto bias) {
       constexpr bool CAP = decltype(cap)::value, BIAS = decltype(bias)::value;
-      int si = 0, r = 0;
+      int si = si0, r = r0, st = 0;
+      uint32_t ph = 0;
       for (int j = 0; j < nj; ++j) {
-        float* sL = wL + (j & 1) * 4 * TQJ;
-        float* sD = sL + TQJ;
-        int* sB = reinterpret_cast<int*>(sD + TQJ);
-        int* sE = sB + TQJ;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int c = lane + 32 * h;
-          if (c < TQJ) {
-            sL[c] = nl[h];
-            sD[c] = nd[h];
-            sB[c] = jb[h];
-            sE[c] = je[h];
-          }
-        }
-        const bool all_live = whole(jb, je);
-        __syncwarp();  // this warp's buffer is complete (the other is two jobs old)
+        const float* sL = reinterpret_cast<const float*>(sStat + st * K::STAT_BYTES);
+        const float* sD = sL + TQJ;
+        const int* sB = reinterpret_cast<const int*>(sD + TQJ);
+        const int* sE = sB + TQJ;
         const float slope2 = BIAS ? P.slopes[stream_of(si)] * kLog2e : 0.f;
-        const float d0 = (float)((qt0 + r) * TQJ - u);
+        const int qa = (qt0 + r) * TQJ;  // the job's first query
+        const float d0 = (float)(qa - u);
         if (++r == per) {
           r = 0;
           ++si;
         }
-        if (j + 1 < nj) fetch(si, qt0 + r);
+        if (!warp_wait(&r_clean[st], ph, P)) { ok = false; break; }
+        const bool all_live = sE[TQJ] != 0;
+        if (++st == K::STAGES) {
+          st = 0;
+          ph ^= 1;
+        }
         if (!warp_wait(sdp_full, j & 1, P)) { ok = false; break; }
         tc_fence_after();
         uint32_t pp[TQJ / 2], pd[TQJ / 2];
         {
-          uint32_t sr[TQJ], dr[TQJ];
-          tmem_ldN_wait<TQJ>(t_base + K::S_COL, sr);
+          float sr[TQJ];
+          uint32_t dr[TQJ];
+          {
+            uint32_t r[TQJ];
+            tmem_ldN_wait<TQJ>(t_base + K::S_COL, r);
+#pragma unroll
+            for (int c = 0; c < TQJ; ++c) sr[c] = __uint_as_float(r[c]);
+          }
           tmem_ldN_wait<TQJ>(t_base + K::DP_COL, dr);
           if (j + 1 < nj) {
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(s_free);
           }
-          auto one = [&](int c, float L, float D, float& p, float& d) {
-            float dc;
-            const float z =
-                score<CAP, BIAS>(P, __uint_as_float(sr[c]), slope2, d0 + (float)c, dc);
-            p = ex2(z - L);
-            d = p * (__uint_as_float(dr[c]) - D);
-            if (CAP) d *= dc;
-          };
-          if (all_live) {
+          const bool poly = !CAP || !__any_sync(0xffffffffu, !(abs_max<TQJ>(sr) < P.cap.limit));
+          const float in = CAP ? P.cap.log2 : P.scale_log2;
+          const float2 in2 = make_float2(in, in);
+          const bool linear = !BIAS || qa >= u1 - 1;  // every query at or behind every key
+          const float2 step = make_float2(-8.f * slope2, -8.f * slope2);
+          float2 chain[4];  // the linear bias of four pairs, eight queries a step
 #pragma unroll
-            for (int x4 = 0; x4 < TQJ / 4; ++x4) {
-              const float4 L4 = reinterpret_cast<const float4*>(sL)[x4];
-              const float4 D4 = reinterpret_cast<const float4*>(sD)[x4];
-              float p[4], d[4];
-              one(4 * x4, L4.x, D4.x, p[0], d[0]);
-              one(4 * x4 + 1, L4.y, D4.y, p[1], d[1]);
-              one(4 * x4 + 2, L4.z, D4.z, p[2], d[2]);
-              one(4 * x4 + 3, L4.w, D4.w, p[3], d[3]);
-              pp[2 * x4] = pack_bf16x2(p[0], p[1]);
-              pp[2 * x4 + 1] = pack_bf16x2(p[2], p[3]);
-              pd[2 * x4] = pack_bf16x2(d[0], d[1]);
-              pd[2 * x4 + 1] = pack_bf16x2(d[2], d[3]);
-            }
-          } else {
+          for (int i = 0; i < 4; ++i)
+            chain[i] = make_float2(-slope2 * (d0 + (float)(2 * i)), -slope2 * (d0 + (float)(2 * i + 1)));
+          auto all = [&](auto pl) {
 #pragma unroll
-            for (int x = 0; x < TQJ / 2; ++x) {
-              float p[2], d[2];
+          for (int x4 = 0; x4 < TQJ / 4; ++x4) {
+            const float4 L4 = reinterpret_cast<const float4*>(sL)[x4];  // -lse
+            const float4 D4 = reinterpret_cast<const float4*>(sD)[x4];  // -D
+            const float2 nL[2] = {make_float2(L4.x, L4.y), make_float2(L4.z, L4.w)};
+            const float2 nD[2] = {make_float2(D4.x, D4.y), make_float2(D4.z, D4.w)};
+            float2 p[2], d[2];
 #pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const int c = 2 * x + e;
-                const float D = sD[c];
-                one(c, sL[c], D, p[e], d[e]);
-                // a row whose dout was cleaned has an infinite or NaN D, which p takes on
-                p[e] = fmaf(0.f, D, p[e]);
-                const bool in = key_ok && u >= sB[c] && u < sE[c];
-                p[e] = in ? p[e] : 0.f;
-                d[e] = in ? d[e] : 0.f;
+            for (int h = 0; h < 2; ++h) {
+              const int c = 4 * x4 + 2 * h;
+              float2 v = make_float2(sr[c], sr[c + 1]);
+              if constexpr (CAP) v = cap_tanh<decltype(pl)::value>(P.cap, v);
+              float2 b = nL[h];
+              if constexpr (BIAS) {
+                if (linear) {
+                  b = add2(b, chain[(c >> 1) & 3]);
+                  chain[(c >> 1) & 3] = add2(chain[(c >> 1) & 3], step);
+                } else {
+                  b.x = fmaf(-slope2, fabsf(d0 + (float)c), b.x);
+                  b.y = fmaf(-slope2, fabsf(d0 + (float)(c + 1)), b.y);
+                }
               }
-              pp[x] = pack_bf16x2(p[0], p[1]);
-              pd[x] = pack_bf16x2(d[0], d[1]);
+              const float2 t = fma2(v, in2, b);
+              p[h] = ((c >> 1) & 7) >= 8 - kBwdFma<CAP, BIAS> ? exp2_fma2_nan(t)
+                                                              : make_float2(ex2(t.x), ex2(t.y));
+              d[h] = mul2(p[h], add2(make_float2(__uint_as_float(dr[c]),
+                                                 __uint_as_float(dr[c + 1])), nD[h]));
+              if constexpr (CAP)
+                d[h] = mul2(d[h], fma2(mul2(v, v), make_float2(-1.f, -1.f), make_float2(1.f, 1.f)));
             }
+            if (!all_live) {
+              const int4 B4 = reinterpret_cast<const int4*>(sB)[x4];
+              const int4 E4 = reinterpret_cast<const int4*>(sE)[x4];
+              const bool in0 = u >= B4.x && u < E4.x, in1 = u >= B4.y && u < E4.y;
+              const bool in2b = u >= B4.z && u < E4.z, in3 = u >= B4.w && u < E4.w;
+              // a row whose dout was cleaned has an infinite or NaN D, which p takes on
+              p[0].x = in0 ? fmaf(0.f, nD[0].x, p[0].x) : 0.f;
+              p[0].y = in1 ? fmaf(0.f, nD[0].y, p[0].y) : 0.f;
+              p[1].x = in2b ? fmaf(0.f, nD[1].x, p[1].x) : 0.f;
+              p[1].y = in3 ? fmaf(0.f, nD[1].y, p[1].y) : 0.f;
+              d[0].x = in0 ? d[0].x : 0.f;
+              d[0].y = in1 ? d[0].y : 0.f;
+              d[1].x = in2b ? d[1].x : 0.f;
+              d[1].y = in3 ? d[1].y : 0.f;
+            }
+            pp[2 * x4] = pack_bf16x2(p[0].x, p[0].y);
+            pp[2 * x4 + 1] = pack_bf16x2(p[1].x, p[1].y);
+            pd[2 * x4] = pack_bf16x2(d[0].x, d[0].y);
+            pd[2 * x4 + 1] = pack_bf16x2(d[1].x, d[1].y);
           }
+          };
+          if (CAP && !poly) all(std::integral_constant<bool, false>{});
+          else all(std::integral_constant<bool, true>{});
         }
         // the previous job's products have read p^T and dz^T
         if (j > 0 && !warp_wait(d_free, (j - 1) & 1, P)) { ok = false; break; }
@@ -904,9 +993,9 @@ attn_scores_dkdv_kernel(const __grid_constant__ Params P) {
       }
     });
     if (ok && nj > 0) ok = warp_wait(acc_full, 0, P);
-    if (ok) {
-      tc_fence_after();
-      const int64_t tok = (int64_t)b_idx * P.T + u;
+    tc_fence_after();
+    const int64_t tok = (int64_t)b_idx * P.T + u;
+    if (P.split == 1 && ok) {
       __nv_bfloat16* dk = P.dk + (int64_t)g * P.dk_hs + tok * P.dk_ts;
       __nv_bfloat16* dv = P.dv + (int64_t)g * P.dv_hs + tok * P.dv_ts;
       if (nj > 0) {
@@ -915,6 +1004,67 @@ attn_scores_dkdv_kernel(const __grid_constant__ Params P) {
       } else if (key_ok) {
         zero_row<DH>(dk);
         zero_row<DH>(dv);
+      }
+    }
+  }
+  if (P.split > 1) {
+    // The cluster's CTAs hold partial sums of the same rows of [dV | dK]. Each takes one part
+    // of the columns: it receives the others' values of them in its own shared memory (the
+    // tiles there have been read) and adds the parts in rank order.
+    cluster_sync();  // every CTA's products are done
+    const int cols = 2 * DH / P.split;  // columns of a part, a multiple of 8
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t t_acc = tmem + ((uint32_t)((warp & 3) * 32) << 16) + K::DV_COL;
+    if (warp >= 4) {
+      for (int p = 0; p < P.split; ++p) {
+        if (p == part) continue;
+        const int slot = part < p ? part : part - 1;
+        const uint32_t dst = map_shared(smem_u32(smem) + (slot * cols / 4 * 128 + row) * 16, p);
+        for (int c = 0; c < cols; c += 8) {
+          uint32_t v[8];
+          tmem_ld8_wait(t_acc + p * cols + c, v);
+          if (nj == 0) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = 0u;
+          }
+          st_cluster_v4(dst + c / 4 * 2048, v);
+          st_cluster_v4(dst + (c / 4 + 1) * 2048, v + 4);
+        }
+      }
+    }
+    cluster_sync();  // all parts have arrived
+    if (warp >= 4) {
+      const int u = u0 + row;
+      const bool key_ok = u < P.T;
+      const int64_t tok = (int64_t)b_idx * P.T + u;
+      const float4* got = reinterpret_cast<const float4*>(smem);
+      for (int c = 0; c < cols; c += 8) {
+        uint32_t v[8];
+        tmem_ld8_wait(t_acc + part * cols + c, v);
+        float sum[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum[i] = 0.f;
+        for (int p = 0; p < P.split; ++p) {
+          if (p == part) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum[i] += nj == 0 ? 0.f : __uint_as_float(v[i]);
+          } else {
+            const int slot = p < part ? p : p - 1;
+            const float4 x = got[(slot * cols + c) / 4 * 128 + row];
+            const float4 y = got[((slot * cols + c) / 4 + 1) * 128 + row];
+            sum[0] += x.x; sum[1] += x.y; sum[2] += x.z; sum[3] += x.w;
+            sum[4] += y.x; sum[5] += y.y; sum[6] += y.z; sum[7] += y.w;
+          }
+        }
+        const int col = part * cols + c;
+        const bool is_k = col >= DH;
+        const float sc = is_k ? P.scale : 1.f;
+        __nv_bfloat16* dst = is_k ? P.dk + (int64_t)g * P.dk_hs + tok * P.dk_ts + (col - DH)
+                                  : P.dv + (int64_t)g * P.dv_hs + tok * P.dv_ts + col;
+        if (key_ok)
+          *reinterpret_cast<uint4*>(dst) =
+              make_uint4(pack_bf16x2(sum[0] * sc, sum[1] * sc), pack_bf16x2(sum[2] * sc, sum[3] * sc),
+                         pack_bf16x2(sum[4] * sc, sum[5] * sc), pack_bf16x2(sum[6] * sc, sum[7] * sc));
       }
     }
   }
@@ -965,10 +1115,13 @@ int launch_dh(const AttnArgs& a, cudaStream_t st) {
   P.nq = (a.T + TQ - 1) / TQ;
   P.scale = a.scale;
   P.scale_log2 = a.scale * kLog2e;
-  P.cap_in = a.softcap > 0.f ? 2.f * a.scale * kLog2e / a.softcap : 0.f;
-  P.cap_log2 = a.softcap * kLog2e;
+  P.cap = cap_form(a.scale, a.softcap);
   P.status = a.status;
   P.spin = a.spin > 0 ? a.spin : (int64_t)1 << 22;
+  int dev = 0, num_sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&num_sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return -1;
   int n = 0;
   if (!a.dsum_given || masked) {
     const dim3 grid((unsigned)(a.B * (int64_t)P.nq), a.dsum_given ? 1 : a.S);
@@ -991,9 +1144,34 @@ int launch_dh(const AttnArgs& a, cudaStream_t st) {
       !tmap_heads(&P.tm_k, a.kk, a.B, a.T, DH, C::CW, TK, sw) ||
       !tmap_heads(&P.tm_v, a.v, a.B, a.T, DH, C::CW, TK, sw))
     return -1;
-  if (launch_pdl(attn_scores_dkdv_kernel<DH>, dim3((unsigned)((int64_t)a.B * a.G * P.nq)),
-                 dim3(THREADS), K::SMEM, st, P) != cudaSuccess)
-    return -1;
+  // Under a causal mask the first key tiles have by far the most jobs, and head 0 has the
+  // shared stream's too: one CTA per tile would leave most of the grid waiting for a few. Tiles
+  // are split over clusters while the grid holds fewer than two items per resident CTA (one
+  // where an SM holds a single CTA: nothing then hides a CTA's start and the cluster's sum)
+  // and every CTA keeps at least four jobs. 8192 causal tokens at d_h 48: 592 us of backward
+  // without the split, 443 with this rule, 472 at twice as much; at d_h 128, 2 x 2048 tokens
+  // in a window: 110, 110, 193.
+  const int64_t items = (int64_t)a.B * a.G * P.nq;
+  const int64_t jobs = (int64_t)(a.k + (a.S > a.G * a.k ? 1 : 0)) * ((a.T + K::TQJ - 1) / K::TQJ);
+  P.split = 1;
+  while (P.split < kMaxSplit && items * P.split < (C::CTAS == 2 ? 4 : 1) * (int64_t)num_sms &&
+         jobs >= 8 * P.split)
+    P.split *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(items * P.split));
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = K::SMEM;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)P.split;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = P.split > 1 ? 2 : 1;
+  if (cudaLaunchKernelEx(&cfg, attn_scores_dkdv_kernel<DH>, P) != cudaSuccess) return -1;
   return n + 1;
 }
 
