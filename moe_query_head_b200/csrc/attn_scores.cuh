@@ -87,15 +87,17 @@ __device__ __forceinline__ float tanh_from_2log2(float x2) {
   return fmaf(-2.f, rcp_approx(ex2(x2) + 1.f), 1.f);
 }
 
-// The cap's tanh of a pair of scores. An odd polynomial of degree 9 on the FMA pipe serves
-// scores whose tanh argument lies in [-1, 1] (the ordinary case: caps are chosen above the
-// scores); others take the exponential and a reciprocal, 16 cycles of the MUFU unit per score
-// and warp against the polynomial's 6 of the FMA pipe. x Q(x^2) was fitted for minimal largest
-// relative error on [0, 1] (iteratively reweighted least squares): 7e-6 in float32, which
-// moves a weight by less than a tenth of its bf16 step at a cap of 50. The host folds the
-// scores' factor into the coefficients, so the raw score is the polynomial's argument.
+// The cap's tanh of a pair of scores. An odd polynomial of degree 7 on the FMA pipe serves
+// scores up to three quarters of the cap (the ordinary case: caps are chosen above the scores);
+// a warp that meets larger ones takes the exponential and a reciprocal for its tile, 16 cycles
+// of the MUFU unit per score and warp against the polynomial's 5 of the FMA pipe. x Q(x^2)
+// was fitted for minimal largest relative error on [0, 3/4] (iteratively reweighted least
+// squares): 1.1e-5, which moves a weight by a tenth of its bf16 half step at most at a cap of
+// 50. (Degree 9 up to the cap itself: one more FMA per score, no faster where scores are
+// large.) The host folds the scores' factor into the coefficients, so the raw score is the
+// polynomial's argument.
 struct CapForm {
-  float2 c[5];   // Q's coefficients times factor^(2 i + 1), each twice
+  float2 c[4];   // Q's coefficients times factor^(2 i + 1), each twice
   float limit;   // largest |score| the polynomial serves
   float t2;      // factor 2 log2(e): the argument of tanh_from_2log2
   float log2;    // softcap log2(e)
@@ -104,15 +106,15 @@ struct CapForm {
 inline CapForm cap_form(float scale, float softcap) {
   CapForm f = {};
   if (!(softcap > 0.f)) return f;
-  const double q[5] = {0.9999930893856743, -0.33298065253491427, 0.13036811257418396,
-                       -0.04481755463875348, 0.009036424252608788};
+  const double q[4] = {0.9999889837677725, -0.3326967088343551, 0.12742696990927016,
+                       -0.03545278562805266};
   const double x = (double)scale / softcap;
   double power = x;
-  for (int i = 0; i < 5; ++i) {
+  for (int i = 0; i < 4; ++i) {
     f.c[i] = make_float2((float)(q[i] * power), (float)(q[i] * power));
     power *= x * x;
   }
-  f.limit = (float)(1.0 / x);
+  f.limit = (float)(0.75 / x);
   f.t2 = (float)(x * 2.8853900817779268);
   f.log2 = softcap * 1.4426950408889634f;
   f.on = 1;
@@ -124,8 +126,7 @@ template <bool POLY>
 __device__ __forceinline__ float2 cap_tanh(const CapForm& f, float2 s) {
   if constexpr (POLY) {
     const float2 y = mul2(s, s);
-    float2 p = fma2(f.c[4], y, f.c[3]);
-    p = fma2(p, y, f.c[2]);
+    float2 p = fma2(f.c[3], y, f.c[2]);
     p = fma2(p, y, f.c[1]);
     p = fma2(p, y, f.c[0]);
     return mul2(p, s);

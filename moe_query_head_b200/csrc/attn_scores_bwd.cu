@@ -464,7 +464,8 @@ attn_scores_dq_kernel(const __grid_constant__ Params P) {
           const bool poly = !CAP || !__any_sync(0xffffffffu, !(abs_max<64>(sr) < P.cap.limit));
           const float in = CAP ? P.cap.log2 : P.scale_log2;
           const float2 in2 = make_float2(in, in), nl2 = make_float2(-lse, -lse);
-          const float2 nD2 = make_float2(-dsum, -dsum);
+          const float Ds = CAP ? dsum : -dsum;
+          const float2 nD2 = make_float2(Ds, Ds), m1 = make_float2(-1.f, -1.f);
           // dz of the scores' columns 2x, 2x + 1, their bias and -lse in b
           auto pair = [&](int x, float2 b, auto pl) {
             float2 v = make_float2(sr[2 * x], sr[2 * x + 1]);
@@ -473,11 +474,11 @@ attn_scores_dq_kernel(const __grid_constant__ Params P) {
             const float2 p = (x & 7) >= 8 - kBwdFma<CAP, BIAS>
                                  ? exp2_fma2_nan(t)
                                  : make_float2(ex2(t.x), ex2(t.y));
-            float2 d = mul2(p, add2(make_float2(__uint_as_float(dr[2 * x]),
-                                                __uint_as_float(dr[2 * x + 1])), nD2));
-            if constexpr (CAP)
-              d = mul2(d, fma2(mul2(v, v), make_float2(-1.f, -1.f), make_float2(1.f, 1.f)));
-            return d;
+            const float2 dp = make_float2(__uint_as_float(dr[2 * x]), __uint_as_float(dr[2 * x + 1]));
+            if constexpr (CAP)  // (1 - tanh^2) (dP - D) = (tanh^2 - 1) (D - dP)
+              return mul2(mul2(p, fma2(dp, m1, nD2)), fma2(v, v, m1));
+            else
+              return mul2(p, add2(dp, nD2));
           };
           const float d0 = (float)(kv0 - q);
           auto all = [&](auto pl) {
@@ -950,10 +951,13 @@ attn_scores_dkdv_kernel(const __grid_constant__ Params P) {
               const float2 t = fma2(v, in2, b);
               p[h] = ((c >> 1) & 7) >= 8 - kBwdFma<CAP, BIAS> ? exp2_fma2_nan(t)
                                                               : make_float2(ex2(t.x), ex2(t.y));
-              d[h] = mul2(p[h], add2(make_float2(__uint_as_float(dr[c]),
-                                                 __uint_as_float(dr[c + 1])), nD[h]));
-              if constexpr (CAP)
-                d[h] = mul2(d[h], fma2(mul2(v, v), make_float2(-1.f, -1.f), make_float2(1.f, 1.f)));
+              const float2 g = add2(make_float2(__uint_as_float(dr[c]), __uint_as_float(dr[c + 1])),
+                                    nD[h]);
+              if constexpr (CAP)  // (1 - tanh^2) g, the sign in the factor -p
+                d[h] = mul2(mul2(g, mul2(p[h], make_float2(-1.f, -1.f))),
+                            fma2(v, v, make_float2(-1.f, -1.f)));
+              else
+                d[h] = mul2(p[h], g);
             }
             if (!all_live) {
               const int4 B4 = reinterpret_cast<const int4*>(sB)[x4];
