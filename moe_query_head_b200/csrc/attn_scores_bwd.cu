@@ -26,6 +26,7 @@
 #include <type_traits>
 
 #include "attn_scores.cuh"
+#include "scores_api.cuh"
 
 namespace gqe {
 namespace {
@@ -1122,10 +1123,8 @@ int launch_dh(const AttnArgs& a, cudaStream_t st) {
   P.cap = cap_form(a.scale, a.softcap);
   P.status = a.status;
   P.spin = a.spin > 0 ? a.spin : (int64_t)1 << 22;
-  int dev = 0, num_sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&num_sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return -1;
+  const int num_sms = current_num_sms();
+  if (num_sms < 0) return -1;
   int n = 0;
   if (!a.dsum_given || masked) {
     const dim3 grid((unsigned)(a.B * (int64_t)P.nq), a.dsum_given ? 1 : a.S);

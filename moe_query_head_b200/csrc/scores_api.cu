@@ -4,6 +4,8 @@
 #include <math.h>
 #include <string.h>
 
+#include <atomic>
+
 #include "attn_scores.cuh"
 #include "attn_scores_decode.cuh"
 #include "scores_api.cuh"
@@ -13,20 +15,34 @@ namespace gqe {
 // The device's status word: what the operators' kernels report (gqe_check_op_status reads it).
 __device__ int32_t g_op_status;
 
+namespace {
+constexpr int kMaxDevices = 64;
+std::atomic<int32_t*> g_status_words[kMaxDevices];  // looked up once per device
+std::atomic<int> g_num_sms[kMaxDevices];
+}  // namespace
+
 int32_t* op_status_word() {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return nullptr;
+  const bool known = dev >= 0 && dev < kMaxDevices;
+  if (known)
+    if (int32_t* p = g_status_words[dev].load(std::memory_order_relaxed)) return p;
   void* p = nullptr;
   if (cudaGetSymbolAddress(&p, g_op_status) != cudaSuccess) {
     cudaGetLastError();
     return nullptr;
   }
+  if (known) g_status_words[dev].store(static_cast<int32_t*>(p), std::memory_order_relaxed);
   return static_cast<int32_t*>(p);
 }
 
 int current_num_sms() {
   int dev = 0, n = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return -1;
+  const bool known = dev >= 0 && dev < kMaxDevices;
+  if (known && (n = g_num_sms[dev].load(std::memory_order_relaxed)) > 0) return n;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return -1;
+  if (known) g_num_sms[dev].store(n, std::memory_order_relaxed);
   return n;
 }
 

@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -301,9 +302,15 @@ def gqe_set_stage_events(h, events) -> None:
 # Operators on the layer's streams, without a handle. Tensors are [heads, tokens, d_h] views
 # with dense rows (any head and token strides that are multiples of 16 bytes); sizes, types
 # and devices are checked here, the rest by the library. Calls run on the tensors' device, on
-# `stream` or that device's current stream.
+# `stream` or that device's current stream. Their structs are packed as bytes, which costs the
+# small calls (one new token per sequence) a third of what ctypes structures do.
 # ----------------------------------------------------------------------------------------
 _DTYPES = {torch.bfloat16: GQE_BF16, torch.float32: GQE_F32}
+_pack_heads = struct.Struct("@Piqq").pack
+_pack_transform = struct.Struct("@iiifPPiiP").pack
+_pack_scores = struct.Struct("@iiiiiiiffPPP").pack
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _require(ok: bool, where: str) -> None:
@@ -311,61 +318,83 @@ def _require(ok: bool, where: str) -> None:
         raise GQEError(GQE_ERR_INVALID_ARG, where)
 
 
-def _heads(t, shape, dtype, device, where: str) -> Heads:
+def _heads(t, shape, dtype, index, where: str) -> bytes:
     """The gqe_heads of a tensor of this shape, type and device with dense rows."""
     st = t.stride()
-    if (t.shape != shape or t.dtype is not dtype or t.device != device
+    if (t.shape != shape or t.dtype is not dtype or t.get_device() != index
             or (st[2] != 1 and t.numel())):
         raise GQEError(GQE_ERR_INVALID_ARG, where)
-    return Heads(t.data_ptr(), shape[0], st[0], st[1])
+    return _pack_heads(t.data_ptr(), shape[0], st[0], st[1])
 
 
-def _cache(t, shape, device, dtype, where: str) -> Heads:
+def _cache(t, shape, dtype, index, where: str) -> bytes:
     """The gqe_heads of a KV cache [G, B, L_max, d_h] with dense rows."""
     st = t.stride()
-    if (t.shape != shape or t.dtype is not dtype or t.device != device
+    if (t.shape != shape or t.dtype is not dtype or t.get_device() != index
             or (t.numel() and (st[3] != 1 or (shape[2] > 1 and st[2] != shape[3])))):
         raise GQEError(GQE_ERR_INVALID_ARG, where)
-    return Heads(t.data_ptr(), shape[0], st[0], st[1])
+    return _pack_heads(t.data_ptr(), shape[0], st[0], st[1])
 
 
-def _vector(t, n, dtype, device, where: str):
-    """Address of a dense vector of n values, or None."""
+def _vector(t, n, dtype, index, where: str) -> int:
+    """Address of a dense vector of n values; 0 (a null pointer) for None."""
     if t is None:
-        return None
-    if t.numel() != n or t.dtype is not dtype or t.device != device or not t.is_contiguous():
+        return 0
+    if (t.numel() != n or t.dtype is not dtype or t.get_device() != index
+            or not t.is_contiguous()):
         raise GQEError(GQE_ERR_INVALID_ARG, where)
     return t.data_ptr()
 
 
-class _On:
-    """The device of a call's tensors made current, and its stream."""
-
-    def __init__(self, device, stream, where):
-        _require(device.type == "cuda", where)
-        self.device = device
-        self.before = torch.cuda.current_device()
-        self.raw = (stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream
-
-    def __enter__(self):
-        if self.device.index != self.before:
-            torch.cuda.set_device(self.device)
-        return self.raw
-
-    def __exit__(self, *exc):
-        if self.device.index != self.before:
-            torch.cuda.set_device(self.before)
-        return False
+def _device(t, where: str) -> int:
+    """The index of a CUDA tensor's device."""
+    index = t.get_device()
+    if index < 0:
+        raise GQEError(GQE_ERR_INVALID_ARG, where)
+    return index
 
 
-def _transform(q, norm, q_weight, k_weight, eps, inv_freq, interleaved, where) -> QkTransform:
-    _require(q.dim() == 3 and q.dtype in _DTYPES, where)
-    d, dev = q.shape[2], q.device
+def _call(fn, index: int, stream, where: str, *args) -> None:
+    """fn(*args, stream) with the tensors' device current."""
+    raw = stream.cuda_stream if stream is not None else _raw_stream(index)
+    if index == torch.cuda.current_device():
+        status = fn(*args, raw)
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, raw)
+    if status != GQE_OK:
+        raise GQEError(status, where)
+
+
+def _scratch(n: int, index: int, stream):
+    """n bytes from torch's allocator, in order with the call's stream."""
+    if stream is None:
+        return torch.empty(n, dtype=torch.uint8, device=index)
+    with torch.cuda.stream(stream):
+        return torch.empty(n, dtype=torch.uint8, device=index)
+
+
+def _room(workspace, size, index: int, stream, where: str):
+    """Address, bytes and owner of a call's scratch: the caller's, or `size` new bytes."""
+    if workspace is None:
+        if not size > 0:
+            return 0, 0, None
+        workspace = _scratch(size, index, stream)
+        return workspace.data_ptr(), size, workspace
+    _require(workspace.get_device() == index and workspace.is_contiguous(), where)
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+
+
+def _transform(q, index, norm, q_weight, k_weight, eps, inv_freq, interleaved, where) -> bytes:
+    if q.dim() != 3 or q.dtype not in _DTYPES:
+        raise GQEError(GQE_ERR_INVALID_ARG, where)
+    d = q.shape[2]
     rot = 0 if inv_freq is None else 2 * inv_freq.numel()
-    return QkTransform(d, _DTYPES[q.dtype], int(norm), eps,
-                       _vector(q_weight, d, torch.float32, dev, where),
-                       _vector(k_weight, d, torch.float32, dev, where), rot, int(interleaved),
-                       _vector(inv_freq, rot // 2, torch.float64, dev, where))
+    return _pack_transform(d, _DTYPES[q.dtype], int(norm), eps,
+                           _vector(q_weight, d, torch.float32, index, where),
+                           _vector(k_weight, d, torch.float32, index, where), rot,
+                           int(interleaved),
+                           _vector(inv_freq, rot // 2, torch.float64, index, where))
 
 
 def gqe_qk_norm_rope(q, k, q_out, k_out, *, positions=None, T=0, norm=True, q_weight=None,
@@ -374,16 +403,14 @@ def gqe_qk_norm_rope(q, k, q_out, k_out, *, positions=None, T=0, norm=True, q_we
     """RMS norm of every head of q [Hq, M, d_h] and k [Hk, M, d_h] and rotation by position in
     one pass (see include/gqe.h). positions: int32 [M], or None for t % T (T = 0: t)."""
     w = "gqe_qk_norm_rope"
-    tr = _transform(q, norm, q_weight, k_weight, eps, inv_freq, interleaved, w)
-    dt, dev, sq, M = q.dtype, q.device, q.shape, q.shape[1]
-    sk = torch.Size((k.shape[0], M, sq[2]))
-    hq, hk = _heads(q, sq, dt, dev, w), _heads(k, sk, dt, dev, w)
-    oq, ok = _heads(q_out, sq, dt, dev, w), _heads(k_out, sk, dt, dev, w)
-    pos = _vector(positions, M, torch.int32, dev, w)
-    ref = ctypes.byref
-    with _On(dev, stream, w) as st:
-        _check(lib.gqe_qk_norm_rope(ref(tr), M, ref(hq), ref(hk), pos, T or max(M, 1), ref(oq),
-                                    ref(ok), st), w)
+    i = _device(q, w)
+    tr = _transform(q, i, norm, q_weight, k_weight, eps, inv_freq, interleaved, w)
+    dt, sq = q.dtype, q.shape
+    M = sq[1]
+    sk = (k.shape[0], M, sq[2])
+    _call(lib.gqe_qk_norm_rope, i, stream, w, tr, M, _heads(q, sq, dt, i, w),
+          _heads(k, sk, dt, i, w), _vector(positions, M, torch.int32, i, w), T or max(M, 1),
+          _heads(q_out, sq, dt, i, w), _heads(k_out, sk, dt, i, w))
 
 
 def gqe_qk_norm_rope_backward(q, k, dq_out, dk_out, dq, dk, dq_weight=None, dk_weight=None, *,
@@ -393,38 +420,19 @@ def gqe_qk_norm_rope_backward(q, k, dq_out, dk_out, dq, dk, dq_weight=None, dk_w
     """Gradients of gqe_qk_norm_rope given its inputs and the gradients of its outputs (see
     include/gqe.h); dq_weight, dk_weight: float32 [d_h] to fill, or None."""
     w = "gqe_qk_norm_rope_backward"
-    tr = _transform(q, norm, q_weight, k_weight, eps, inv_freq, interleaved, w)
-    dt, dev, sq, M = q.dtype, q.device, q.shape, q.shape[1]
-    sk = torch.Size((k.shape[0], M, sq[2]))
-    hq, hk = _heads(q, sq, dt, dev, w), _heads(k, sk, dt, dev, w)
-    gq, gk = _heads(dq_out, sq, dt, dev, w), _heads(dk_out, sk, dt, dev, w)
-    oq, ok = _heads(dq, sq, dt, dev, w), _heads(dk, sk, dt, dev, w)
-    pos = _vector(positions, M, torch.int32, dev, w)
-    wq = _vector(dq_weight, sq[2], torch.float32, dev, w)
-    wk = _vector(dk_weight, sq[2], torch.float32, dev, w)
-    ref = ctypes.byref
-    with _On(dev, stream, w) as st:
-        if workspace is None and norm and (wq or wk):
-            n = max(0, lib.gqe_qk_norm_rope_workspace_bytes(sq[2]))
-            workspace = _scratch(n, dev, stream)
-        _check(lib.gqe_qk_norm_rope_backward(
-            ref(tr), M, ref(hq), ref(hk), pos, T or max(M, 1), ref(gq), ref(gk), ref(oq),
-            ref(ok), wq, wk, *_room(workspace, dev, w), st), w)
-
-
-def _scratch(n: int, device, stream):
-    """n bytes from torch's allocator, in order with the call's stream."""
-    if stream is None:
-        return torch.empty(n, dtype=torch.uint8, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(n, dtype=torch.uint8, device=device)
-
-
-def _room(workspace, device, where: str):
-    if workspace is None:
-        return None, 0
-    _require(workspace.device == device and workspace.is_contiguous(), where)
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    i = _device(q, w)
+    tr = _transform(q, i, norm, q_weight, k_weight, eps, inv_freq, interleaved, w)
+    dt, sq = q.dtype, q.shape
+    M, d = sq[1], sq[2]
+    sk = (k.shape[0], M, d)
+    wq = _vector(dq_weight, d, torch.float32, i, w)
+    wk = _vector(dk_weight, d, torch.float32, i, w)
+    size = lib.gqe_qk_norm_rope_workspace_bytes(d) if norm and (wq or wk) else 0
+    room, size, owner = _room(workspace, size, i, stream, w)
+    _call(lib.gqe_qk_norm_rope_backward, i, stream, w, tr, M, _heads(q, sq, dt, i, w),
+          _heads(k, sk, dt, i, w), _vector(positions, M, torch.int32, i, w), T or max(M, 1),
+          _heads(dq_out, sq, dt, i, w), _heads(dk_out, sk, dt, i, w), _heads(dq, sq, dt, i, w),
+          _heads(dk, sk, dt, i, w), wq, wk, room, size)
 
 
 def gqe_qk_norm_rope_append(q, k, v, lengths, q_out, k_cache, v_cache, *, norm=True,
@@ -434,28 +442,27 @@ def gqe_qk_norm_rope_append(q, k, v, lengths, q_out, k_cache, v_cache, *, norm=T
     positions `lengths` (int32 [B]; -1: idle slot); k and v go to row lengths[b] of the caches
     [G, B, L_max, d_h] (see include/gqe.h)."""
     w = "gqe_qk_norm_rope_append"
-    tr = _transform(q, norm, q_weight, k_weight, eps, inv_freq, interleaved, w)
-    _require(k_cache.dim() == 4, w)
-    dt, dev, sq, B = q.dtype, q.device, q.shape, q.shape[1]
-    G, L = k.shape[0], k_cache.shape[2]
-    sk = torch.Size((G, B, sq[2]))
-    sc = torch.Size((G, B, L, sq[2]))
-    hq, hk, hv = _heads(q, sq, dt, dev, w), _heads(k, sk, dt, dev, w), _heads(v, sk, dt, dev, w)
-    oq = _heads(q_out, sq, dt, dev, w)
-    ck, cv = _cache(k_cache, sc, dev, dt, w), _cache(v_cache, sc, dev, dt, w)
-    pos = _vector(lengths, B, torch.int32, dev, w)
-    ref = ctypes.byref
-    with _On(dev, stream, w) as st:
-        _check(lib.gqe_qk_norm_rope_append(ref(tr), B, ref(hq), ref(hk), ref(hv), pos, L, ref(oq),
-                                           ref(ck), ref(cv), st), w)
+    i = _device(q, w)
+    tr = _transform(q, i, norm, q_weight, k_weight, eps, inv_freq, interleaved, w)
+    sc = k_cache.shape
+    if len(sc) != 4:
+        raise GQEError(GQE_ERR_INVALID_ARG, w)
+    dt, sq = q.dtype, q.shape
+    B, d = sq[1], sq[2]
+    sk = (k.shape[0], B, d)
+    sc = (k.shape[0], B, sc[2], d)
+    _call(lib.gqe_qk_norm_rope_append, i, stream, w, tr, B, _heads(q, sq, dt, i, w),
+          _heads(k, sk, dt, i, w), _heads(v, sk, dt, i, w),
+          _vector(lengths, B, torch.int32, i, w), sc[2], _heads(q_out, sq, dt, i, w),
+          _cache(k_cache, sc, dt, i, w), _cache(v_cache, sc, dt, i, w))
 
 
-def _scores(q, G, B, T, top_k, causal, scale, softcap, slopes, key_begin, key_end, rows, where):
-    S, dev = q.shape[0], q.device
-    return Scores(B, T, G, top_k, S, q.shape[2], int(causal), scale, softcap,
-                  _vector(slopes, S, torch.float32, dev, where),
-                  _vector(key_begin, rows, torch.int32, dev, where),
-                  _vector(key_end, rows, torch.int32, dev, where))
+def _scores(sq, i, G, B, T, top_k, causal, scale, softcap, slopes, key_begin, key_end, rows,
+            where) -> bytes:
+    return _pack_scores(B, T, G, top_k, sq[0], sq[2], int(causal), scale, softcap,
+                        _vector(slopes, sq[0], torch.float32, i, where),
+                        _vector(key_begin, rows, torch.int32, i, where),
+                        _vector(key_end, rows, torch.int32, i, where))
 
 
 def gqe_attention_forward(q, k, v, out, lse, B, T, top_k, *, causal=True, scale=0.0, softcap=0.0,
@@ -464,18 +471,17 @@ def gqe_attention_forward(q, k, v, out, lse, B, T, top_k, *, causal=True, scale=
     G top_k + 1 with the shared stream) with capped, biased and masked scores; lse: float32
     [S, B T] to fill for the backward pass, or None (see include/gqe.h)."""
     w = "gqe_attention_forward"
-    _require(q.dim() == 3 and k.dim() == 3, w)
-    dev, sq, bf = q.device, q.shape, torch.bfloat16
+    i = _device(q, w)
+    sq, sk, bf = q.shape, k.shape, torch.bfloat16
     M = B * T
-    _require(sq[1] == M, w)
-    a = _scores(q, k.shape[0], B, T, top_k, causal, scale, softcap, slopes, key_begin, key_end, M, w)
-    sk = torch.Size((k.shape[0], M, sq[2]))
-    hq, hk, hv = _heads(q, sq, bf, dev, w), _heads(k, sk, bf, dev, w), _heads(v, sk, bf, dev, w)
-    ho = _heads(out, sq, bf, dev, w)
-    pl = _vector(lse, sq[0] * M, torch.float32, dev, w)
-    ref = ctypes.byref
-    with _On(dev, stream, w) as st:
-        _check(lib.gqe_attention_forward(ref(a), ref(hq), ref(hk), ref(hv), ref(ho), pl, st), w)
+    if len(sq) != 3 or len(sk) != 3 or sq[1] != M:
+        raise GQEError(GQE_ERR_INVALID_ARG, w)
+    G = sk[0]
+    sk = (G, M, sq[2])
+    a = _scores(sq, i, G, B, T, top_k, causal, scale, softcap, slopes, key_begin, key_end, M, w)
+    _call(lib.gqe_attention_forward, i, stream, w, a, _heads(q, sq, bf, i, w),
+          _heads(k, sk, bf, i, w), _heads(v, sk, bf, i, w), _heads(out, sq, bf, i, w),
+          _vector(lse, sq[0] * M, torch.float32, i, w))
 
 
 def gqe_attention_backward(q, k, v, out, lse, dout, dq, dk, dv, B, T, top_k, *, causal=True,
@@ -484,23 +490,19 @@ def gqe_attention_backward(q, k, v, out, lse, dout, dq, dk, dv, B, T, top_k, *, 
     """Gradients dq, dk, dv of gqe_attention_forward (same arguments), given its out and lse and
     the upstream gradient dout (see include/gqe.h)."""
     w = "gqe_attention_backward"
-    _require(q.dim() == 3 and k.dim() == 3, w)
-    dev, sq, bf = q.device, q.shape, torch.bfloat16
+    i = _device(q, w)
+    sq, sk, bf = q.shape, k.shape, torch.bfloat16
     M = B * T
-    _require(sq[1] == M, w)
-    a = _scores(q, k.shape[0], B, T, top_k, causal, scale, softcap, slopes, key_begin, key_end, M, w)
-    sk = torch.Size((k.shape[0], M, sq[2]))
-    hq, hk, hv = _heads(q, sq, bf, dev, w), _heads(k, sk, bf, dev, w), _heads(v, sk, bf, dev, w)
-    ho, hd = _heads(out, sq, bf, dev, w), _heads(dout, sq, bf, dev, w)
-    gq, gk, gv = _heads(dq, sq, bf, dev, w), _heads(dk, sk, bf, dev, w), _heads(dv, sk, bf, dev, w)
-    pl = _vector(lse, sq[0] * M, torch.float32, dev, w)
-    ref = ctypes.byref
-    with _On(dev, stream, w) as st:
-        if workspace is None:
-            workspace = _scratch(max(0, lib.gqe_attention_workspace_bytes(ref(a))), dev, stream)
-        _check(lib.gqe_attention_backward(ref(a), ref(hq), ref(hk), ref(hv), ref(ho), pl, ref(hd),
-                                          ref(gq), ref(gk), ref(gv), *_room(workspace, dev, w),
-                                          st), w)
+    if len(sq) != 3 or len(sk) != 3 or sq[1] != M:
+        raise GQEError(GQE_ERR_INVALID_ARG, w)
+    G = sk[0]
+    sk = (G, M, sq[2])
+    a = _scores(sq, i, G, B, T, top_k, causal, scale, softcap, slopes, key_begin, key_end, M, w)
+    room, size, owner = _room(workspace, lib.gqe_attention_workspace_bytes(a), i, stream, w)
+    _call(lib.gqe_attention_backward, i, stream, w, a, _heads(q, sq, bf, i, w),
+          _heads(k, sk, bf, i, w), _heads(v, sk, bf, i, w), _heads(out, sq, bf, i, w),
+          _vector(lse, sq[0] * M, torch.float32, i, w), _heads(dout, sq, bf, i, w),
+          _heads(dq, sq, bf, i, w), _heads(dk, sk, bf, i, w), _heads(dv, sk, bf, i, w), room, size)
 
 
 def gqe_attention_decode(q, k_cache, v_cache, lengths, out, top_k, *, scale=0.0, softcap=0.0,
@@ -508,21 +510,18 @@ def gqe_attention_decode(q, k_cache, v_cache, lengths, out, top_k, *, scale=0.0,
     """The single-token form: q [S, B, d_h] at positions `lengths` (int32 [B]; -1: no key) over
     rows key_begin[b] .. lengths[b] of the caches [G, B, L_max, d_h] (see include/gqe.h)."""
     w = "gqe_attention_decode"
-    _require(q.dim() == 3 and k_cache.dim() == 4, w)
-    dev, sq, bf = q.device, q.shape, torch.bfloat16
-    G, B, L = k_cache.shape[0], sq[1], k_cache.shape[2]
-    a = _scores(q, G, B, 1, top_k, 1, scale, softcap, slopes, key_begin, None, B, w)
-    sc = torch.Size((G, B, L, sq[2]))
-    hq, ho = _heads(q, sq, bf, dev, w), _heads(out, sq, bf, dev, w)
-    ck, cv = _cache(k_cache, sc, dev, bf, w), _cache(v_cache, sc, dev, bf, w)
-    pos = _vector(lengths, B, torch.int32, dev, w)
-    ref = ctypes.byref
-    with _On(dev, stream, w) as st:
-        if workspace is None:
-            workspace = _scratch(max(0, lib.gqe_attention_decode_workspace_bytes(ref(a), L)), dev,
-                                 stream)
-        _check(lib.gqe_attention_decode(ref(a), ref(hq), ref(ck), ref(cv), L, pos, ref(ho),
-                                        *_room(workspace, dev, w), st), w)
+    i = _device(q, w)
+    sq, sc, bf = q.shape, k_cache.shape, torch.bfloat16
+    if len(sq) != 3 or len(sc) != 4:
+        raise GQEError(GQE_ERR_INVALID_ARG, w)
+    G, B, L = sc[0], sq[1], sc[2]
+    sc = (G, B, L, sq[2])
+    a = _scores(sq, i, G, B, 1, top_k, 1, scale, softcap, slopes, key_begin, None, B, w)
+    room, size, owner = _room(workspace, lib.gqe_attention_decode_workspace_bytes(a, L), i, stream,
+                              w)
+    _call(lib.gqe_attention_decode, i, stream, w, a, _heads(q, sq, bf, i, w),
+          _cache(k_cache, sc, bf, i, w), _cache(v_cache, sc, bf, i, w), L,
+          _vector(lengths, B, torch.int32, i, w), _heads(out, sq, bf, i, w), room, size)
 
 
 def gqe_set_qk_transform(h, d_h=0, dtype=GQE_BF16, *, norm=True, q_weight=None, k_weight=None,
@@ -537,13 +536,13 @@ def gqe_set_qk_transform(h, d_h=0, dtype=GQE_BF16, *, norm=True, q_weight=None, 
     rot = 0 if inv_freq is None else 2 * inv_freq.numel()
 
     def vec(t, n, dt):
-        return None if t is None else _vector(t, n, dt, t.device, w)
+        return 0 if t is None else _vector(t, n, dt, _device(t, w), w)
 
-    tr = QkTransform(d_h, dtype, int(norm), eps, vec(q_weight, d_h, torch.float32),
-                     vec(k_weight, d_h, torch.float32), rot, int(interleaved),
-                     vec(inv_freq, rot // 2, torch.float64))
-    pos = None if positions is None else vec(positions, positions.numel(), torch.int32)
-    _check(lib.gqe_set_qk_transform(h, ctypes.byref(tr), pos, vec(dq_weight, d_h, torch.float32),
+    tr = _pack_transform(d_h, dtype, int(norm), eps, vec(q_weight, d_h, torch.float32),
+                         vec(k_weight, d_h, torch.float32), rot, int(interleaved),
+                         vec(inv_freq, rot // 2, torch.float64))
+    pos = 0 if positions is None else vec(positions, positions.numel(), torch.int32)
+    _check(lib.gqe_set_qk_transform(h, tr, pos, vec(dq_weight, d_h, torch.float32),
                                     vec(dk_weight, d_h, torch.float32)), w)
 
 
@@ -554,7 +553,7 @@ def gqe_set_scores(h, *, scale=0.0, softcap=0.0, slopes=None, key_begin=None,
     w = "gqe_set_scores"
 
     def vec(t, dt):
-        return None if t is None else _vector(t, t.numel(), dt, t.device, w)
+        return 0 if t is None else _vector(t, t.numel(), dt, _device(t, w), w)
 
     _check(lib.gqe_set_scores(h, scale, softcap, vec(slopes, torch.float32),
                               vec(key_begin, torch.int32), vec(key_end, torch.int32)), w)
@@ -563,6 +562,9 @@ def gqe_set_scores(h, *, scale=0.0, softcap=0.0, slopes=None, key_begin=None,
 def gqe_check_op_status(stream=None, device=None) -> int:
     """Synchronises the stream and reads and clears the device's status word of the operators
     above (see include/gqe.h)."""
-    dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
-    with _On(dev, stream, "gqe_check_op_status") as st:
-        return int(lib.gqe_check_op_status(st))
+    index = None if device is None else torch.device(device).index
+    if index is None:
+        index = torch.cuda.current_device()
+    with torch.cuda.device(index):
+        raw = stream.cuda_stream if stream is not None else _raw_stream(index)
+        return int(lib.gqe_check_op_status(raw))
