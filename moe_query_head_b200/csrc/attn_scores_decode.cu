@@ -2,15 +2,22 @@
 // and a first visible key per sequence (the mathematics is in attn_scores.cuh).
 //
 // The work is bound by the cache's bytes (every visible K and V row is read once, for all the
-// query streams of its head), so it runs on CUDA cores. CTA (chunk, KV head, sequence): the
-// sequence's own visible keys are cut into equal chunks, so ragged lengths and windows leave
-// no CTA with more than its share. A chunk streams in tiles of 64 rows through a two-stage
-// cp.async ring in shared memory; each of the four warps takes 16 keys of every tile for all
-// the head's queries: a score per (key, half of the head dims) lane pair, an online softmax
-// over the warp's keys with shuffles, P V with each lane owning pairs of head dimensions. The
-// warps' states are merged in shared memory; with more than one chunk a second kernel, one
-// CTA per (stream, sequence), merges the chunks' states in a fixed order. Rows outside the
-// visible keys are not read: they enter the ring as zeros, so a cache may hold anything there.
+// query streams of its head), with the instruction issue close behind: a score and its part of
+// P V are few operations on few bytes, so it runs on CUDA cores and counts instructions. CTA
+// (chunk, KV head, sequence): the sequence's own visible keys are cut into equal chunks, so
+// ragged lengths and windows leave no CTA with more than its share. A chunk streams in tiles
+// of 64 rows through a three-stage cp.async ring in shared memory (a tile is one contiguous run
+// of memory: thread addresses are constants away from a moving pointer); each of the four
+// warps takes 16 keys of every tile for all the head's queries:
+//   scores  a (key, half of the head dims) pair per lane, packed products in 32 bits;
+//   softmax one warp-wide maximum (redux); the sums stay in the lanes and O is rescaled only
+//           when the maximum grows by more than 2^8;
+//   P V     eight dims per lane, so a key's row takes d_h / 8 lanes and the warp works on
+//           several keys at once; those partial sums are added after the last tile.
+// The warps' states are merged in shared memory. The chunks' are merged by a second kernel,
+// or, where few (sequence, KV head) pairs leave SMs free, by up to eight CTAs of a cluster in
+// the first one's shared memory in the same launch. All merges run in a fixed order. Rows outside the visible keys are not read: they enter the ring as zeros,
+// so a cache may hold anything there.
 #include <string.h>
 
 #include "attn_scores.cuh"
@@ -24,9 +31,10 @@ using namespace tc;
 constexpr int THREADS = 128;
 constexpr int WARPS = THREADS / 32;
 constexpr int TKD = 64;  // keys per tile
-constexpr int STAGES = 2;
+constexpr int STAGES = 3;
 constexpr int MAXQ = kMaxTopK + 1;
 constexpr int KPW = TKD / WARPS;
+constexpr int kMaxCluster = 8;  // chunks merged in shared memory
 
 template <int DH>
 struct Cfg {
@@ -35,12 +43,24 @@ struct Cfg {
   static constexpr bool DENSE = DH % 32 == 16;
   static constexpr int ROWB = DENSE ? DH * 2 : DH * 2 + 16;
   static constexpr int TILE = TKD * ROWB;
-  static constexpr int CHUNKS = DH / 8;
-  static constexpr int NP = (DH / 2 + 31) / 32;  // dim pairs per lane
+  static constexpr int CHUNKS = DH / 8;                       // 16-byte pieces per row
+  static constexpr int PIECES = TKD * CHUNKS / THREADS;       // of a tile, per thread
+  static constexpr int LK = DH / 8;                           // lanes of a key in P V
+  static constexpr int NG = DH == 16 ? 16 : DH == 32 ? 8 : DH <= 64 ? 4 : 2;  // keys at once
   static constexpr int SMEM = STAGES * 2 * TILE + MAXQ * DH * 4;
-  static_assert(STAGES * 2 * TILE >= WARPS * MAXQ * (DH + 2) * 4,
-                "the ring holds the warps' states for the merge");
+  static_assert(STAGES * 2 * TILE >= (WARPS + kMaxCluster) * MAXQ * (DH + 2) * 4,
+                "the ring holds the warps' and the chunks' states for the merges");
+  static_assert(NG * LK <= 32 && KPW % NG == 0, "lanes of P V");
 };
+
+__device__ __forceinline__ float warp_max(float v) {
+  float m;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+  return m;
+}
+__device__ __forceinline__ float2 bf2(uint32_t w) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
 
 __device__ __forceinline__ int stream_of(const DecodeArgs& P, int g, int i) {
   return i < P.k ? g * P.k + i : P.G * P.k;
@@ -62,11 +82,41 @@ __device__ __forceinline__ bool visible(const DecodeArgs& P, int b, int& first, 
   return L >= -1 && L < P.L_max;
 }
 
+// (m, l, O[d]) of query i over the keys of one cluster: the output, or the cluster's state.
+__device__ __forceinline__ void finish_row(const DecodeArgs& P, int g, int i, int b, int part, int d,
+                                           float mx, float lt, float ot) {
+  const int s = stream_of(P, g, i);
+  if (P.np == 1) {
+    out_row(P, s, b)[d] = __float2bfloat16_rn(ot * out_scale(P, s, b, lt));
+    return;
+  }
+  float* slot = P.part + (((int64_t)s * P.B + b) * P.np + part) * (P.d_h + 2);
+  if (d == 0) {
+    slot[0] = mx;
+    slot[1] = lt;
+  }
+  slot[2 + d] = ot;
+}
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// The address of a shared-memory location of this CTA in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t map_shared(uint32_t addr, int rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void st_cluster(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+
 // QMAX: the most queries of a KV head in this launch (2, 4 or 9), a compile-time count so
-// that the per-query state stays in registers; at two queries and d_h <= 48 it fits 64
-// registers and eight CTAs share an SM (more CTAs, more bytes in flight).
+// that the per-query state stays in registers. Four CTAs an SM at two queries and d_h <= 48
+// leave it 128 (64 sequences of 8192 cached tokens, 805 MB: 128 us; six CTAs of 85 registers
+// 167 us, eight of 64 218 us, both spilling; two ring stages instead of three 134 us).
 template <int DH, int QMAX>
-__global__ void __launch_bounds__(THREADS, (DH <= 48 && QMAX <= 2) ? 8 : 1)
+__global__ void __launch_bounds__(THREADS, (DH <= 48 && QMAX <= 2) ? 4 : 1)
 attn_decode_kernel(const __grid_constant__ DecodeArgs P) {
   using C = Cfg<DH>;
   extern __shared__ __align__(16) uint8_t smem[];
@@ -83,25 +133,45 @@ attn_decode_kernel(const __grid_constant__ DecodeArgs P) {
     return;
   }
   const int nq = P.k + (g == 0 && P.S > P.G * P.k ? 1 : 0);
-  // this chunk's keys: the visible ones in nc equal parts, rounded up to whole tiles
-  const int n = max(0, end - first);
-  const int per = (n + P.nc * TKD - 1) / (P.nc * TKD) * TKD;
-  const int k0 = first + min(n, c * per);
-  const int k1 = first + min(n, c * per + per);
+  // this chunk's keys: the visible ones in equal parts, rounded up to whole tiles
+  const int n = max(0, end - first), parts = P.nc * P.np;
+  const int per = (int)(((int64_t)n + parts * TKD - 1) / (parts * TKD)) * TKD;
+  const int k0 = first + (int)min((int64_t)n, (int64_t)c * per);
+  const int k1 = first + (int)min((int64_t)n, (int64_t)c * per + per);
   const __nv_bfloat16* kc = static_cast<const __nv_bfloat16*>(P.kc.data) +
                             g * P.kc.head_stride + (int64_t)b * P.kc.token_stride;
   const __nv_bfloat16* vc = static_cast<const __nv_bfloat16*>(P.vc.data) +
                             g * P.vc.head_stride + (int64_t)b * P.vc.token_stride;
   const int ntiles = (k1 - k0 + TKD - 1) / TKD;
+  // piece i of a tile: 16 bytes at element 8 (tid + 128 i) of the tile's rows
+  kc += (int64_t)k0 * DH + tid * 8;
+  vc += (int64_t)k0 * DH + tid * 8;
+  uint32_t dst[C::PIECES];
+#pragma unroll
+  for (int i = 0; i < C::PIECES; ++i) {
+    const int e = tid + i * THREADS;
+    dst[i] = smem_u32(sK) + (C::DENSE ? e * 16 : e / C::CHUNKS * C::ROWB + e % C::CHUNKS * 16);
+  }
   auto load_tile = [&](int t, int st) {
-    const int base = k0 + t * TKD;
-    for (int e = tid; e < TKD * C::CHUNKS; e += THREADS) {
-      const int r = e / C::CHUNKS, ch = e % C::CHUNKS;
-      const int u = base + r;
-      const int64_t off = (int64_t)min(u, k1 - 1) * DH + ch * 8;
-      const uint32_t bytes = u < k1 ? 16 : 0;
-      cp_async_16(smem_u32(sK + st * C::TILE + r * C::ROWB + ch * 16), kc + off, bytes);
-      cp_async_16(smem_u32(sV + st * C::TILE + r * C::ROWB + ch * 16), vc + off, bytes);
+    const __nv_bfloat16* ks = kc + (int64_t)t * TKD * DH;
+    const __nv_bfloat16* vs = vc + (int64_t)t * TKD * DH;
+    const uint32_t ring = st * C::TILE;
+    if ((t + 1) * TKD <= k1 - k0) {
+#pragma unroll
+      for (int i = 0; i < C::PIECES; ++i) {
+        cp_async_16(dst[i] + ring, ks + i * THREADS * 8, 16);
+        cp_async_16(dst[i] + ring + STAGES * C::TILE, vs + i * THREADS * 8, 16);
+      }
+    } else {
+      // the last tile: rows past the chunk become zeros (their addresses stay inside)
+      const int rows = k1 - k0 - t * TKD;
+#pragma unroll
+      for (int i = 0; i < C::PIECES; ++i) {
+        const bool in = tid + i * THREADS < rows * C::CHUNKS;
+        const int off = in ? i * THREADS * 8 : -tid * 8;
+        cp_async_16(dst[i] + ring, ks + off, in ? 16 : 0);
+        cp_async_16(dst[i] + ring + STAGES * C::TILE, vs + off, in ? 16 : 0);
+      }
     }
   };
   for (int t = 0; t < STAGES - 1; ++t) {
@@ -119,15 +189,18 @@ attn_decode_kernel(const __grid_constant__ DecodeArgs P) {
   constexpr int kHalfXor = C::DENSE ? 1 : 16;  // the lane holding the key's other half
   constexpr int kKeyLane = C::DENSE ? 2 : 1;   // lane stride between keys
   const int krow = warp * KPW + kq;
+  // P V: this lane's key of every NG and its eight dims (lanes without a key repeat key 0's)
+  const int pg = lane / C::LK < C::NG ? lane / C::LK : 0;
+  const uint32_t v_off = (warp * KPW + pg) * C::ROWB + lane % C::LK * 16;
   float m[QMAX], l[QMAX], slope2[QMAX];
-  float2 o[QMAX][C::NP];
+  float2 o[QMAX][4];
 #pragma unroll
   for (int a = 0; a < QMAX; ++a) {
     m[a] = -INFINITY;
     l[a] = 0.f;
     slope2[a] = P.slopes && a < nq ? P.slopes[stream_of(P, g, a)] * kLog2e : 0.f;
 #pragma unroll
-    for (int p = 0; p < C::NP; ++p) o[a][p] = make_float2(0.f, 0.f);
+    for (int p = 0; p < 4; ++p) o[a][p] = make_float2(0.f, 0.f);
   }
   __syncthreads();  // sQ written
   for (int t = 0; t < ntiles; ++t) {
@@ -135,75 +208,60 @@ attn_decode_kernel(const __grid_constant__ DecodeArgs P) {
     cp_async_commit();
     cp_async_wait<STAGES - 1>();
     __syncthreads();  // tile t is in shared memory for every thread
-    const int st = t % STAGES;
-    const uint8_t* kt = sK + st * C::TILE;
-    const uint8_t* vt = sV + st * C::TILE;
+    const uint8_t* kt = sK + t % STAGES * C::TILE + krow * C::ROWB + half * DH;
+    const uint8_t* vt = sV + t % STAGES * C::TILE + v_off;
     const int u = k0 + t * TKD + krow;
     const bool key_ok = u < k1;
     const float dist = (float)(end - 1 - u);  // the new token's position minus the key's
-    float kf[DH / 2];
-    {
-      const uint8_t* row = kt + krow * C::ROWB + half * DH;
+    float2 kf[DH / 4];
 #pragma unroll
-      for (int ch = 0; ch < DH / 16; ++ch) {
-        const uint4 v = *reinterpret_cast<const uint4*>(row + ch * 16);
-        const __nv_bfloat162* p2 = reinterpret_cast<const __nv_bfloat162*>(&v);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float2 f = __bfloat1622float2(p2[e]);
-          kf[ch * 8 + 2 * e] = f.x;
-          kf[ch * 8 + 2 * e + 1] = f.y;
-        }
-      }
+    for (int ch = 0; ch < DH / 16; ++ch) {
+      const uint4 v = *reinterpret_cast<const uint4*>(kt + ch * 16);
+      kf[4 * ch] = bf2(v.x);
+      kf[4 * ch + 1] = bf2(v.y);
+      kf[4 * ch + 2] = bf2(v.z);
+      kf[4 * ch + 3] = bf2(v.w);
     }
 #pragma unroll
     for (int a = 0; a < QMAX; ++a) {
       if (a >= nq) break;  // uniform over the CTA
-      const float* q = sQ + a * DH + half * (DH / 2);
-      float acc = 0.f;
+      const float4* q = reinterpret_cast<const float4*>(sQ + a * DH + half * (DH / 2));
+      float2 acc2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-      for (int d = 0; d < DH / 2; ++d) acc = fmaf(q[d], kf[d], acc);
+      for (int d = 0; d < DH / 8; ++d) {
+        const float4 qv = q[d];
+        acc2[0] = fma2(make_float2(qv.x, qv.y), kf[2 * d], acc2[0]);
+        acc2[1] = fma2(make_float2(qv.z, qv.w), kf[2 * d + 1], acc2[1]);
+      }
+      acc2[0] = add2(acc2[0], acc2[1]);
+      float acc = acc2[0].x + acc2[0].y;
       acc += __shfl_xor_sync(0xffffffffu, acc, kHalfXor);
       if (P.cap_log2 != 0.f) acc = tanh_from_2log2(acc * P.cap_in) * P.cap_log2;
       acc = fmaf(-slope2[a], dist, acc);
       const float sc = key_ok ? acc : -INFINITY;
-      float mt = sc;
+      const float mt = warp_max(sc);
+      if (mt > m[a] + 8.f) {
+        const float alpha = ex2(m[a] - mt);  // 0 from a reference of -inf
+        l[a] *= alpha;
 #pragma unroll
-      for (int off = 8 * kKeyLane; off >= kKeyLane; off >>= 1)
-        mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, off));
-      const float m_new = fmaxf(m[a], mt);
-      // a warp whose keys are all masked so far keeps m = -inf, l = 0, O = 0
-      const float m_ref = m_new == -INFINITY ? 0.f : m_new;
-      const float alpha = ex2(m[a] - m_ref);  // 0 while m is -inf
-      const float pk = ex2(sc - m_ref);       // 0 for a masked key
-      float ps = pk;
-#pragma unroll
-      for (int off = 8 * kKeyLane; off >= kKeyLane; off >>= 1)
-        ps += __shfl_xor_sync(0xffffffffu, ps, off);
-      l[a] = l[a] * alpha + ps;
-      m[a] = m_new;
-#pragma unroll
-      for (int p = 0; p < C::NP; ++p) {
-        o[a][p].x *= alpha;
-        o[a][p].y *= alpha;
+        for (int p = 0; p < 4; ++p) o[a][p] = mul2(o[a][p], make_float2(alpha, alpha));
+        m[a] = mt;
       }
+      // a warp whose keys are all masked so far keeps m = -inf, l = 0, O = 0
+      const float pk = ex2(sc - (m[a] == -INFINITY ? 0.f : m[a]));  // 0 for a masked key
+      l[a] += pk;
 #pragma unroll
-      for (int j = 0; j < KPW; ++j) {
-        const float pj = __shfl_sync(0xffffffffu, pk, j * kKeyLane);
-        const uint8_t* row = vt + (warp * KPW + j) * C::ROWB;
-#pragma unroll
-        for (int p = 0; p < C::NP; ++p) {
-          const int d2 = lane + 32 * p;
-          if (2 * d2 < DH) {
-            const float2 f =
-                __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(row + 4 * d2));
-            o[a][p].x = fmaf(pj, f.x, o[a][p].x);
-            o[a][p].y = fmaf(pj, f.y, o[a][p].y);
-          }
-        }
+      for (int j = 0; j < KPW / C::NG; ++j) {
+        const float pj = __shfl_sync(0xffffffffu, pk, (j * C::NG + pg) * kKeyLane);
+        const uint4 v = *reinterpret_cast<const uint4*>(vt + j * C::NG * C::ROWB);
+        const float2 p2 = make_float2(pj, pj);
+        o[a][0] = fma2(p2, bf2(v.x), o[a][0]);
+        o[a][1] = fma2(p2, bf2(v.y), o[a][1]);
+        o[a][2] = fma2(p2, bf2(v.z), o[a][2]);
+        o[a][3] = fma2(p2, bf2(v.w), o[a][3]);
       }
     }
-    __syncthreads();  // every warp is done with stage st before it is refilled
+    __syncthreads();  // every warp is done with the stage before it is refilled
   }
   cp_async_wait<0>();
   __syncthreads();  // the ring is free: it holds the warps' states for the merge
@@ -212,49 +270,75 @@ attn_decode_kernel(const __grid_constant__ DecodeArgs P) {
   for (int a = 0; a < QMAX; ++a) {
     if (a >= nq) break;
     float* st = sM + (warp * MAXQ + a) * (DH + 2);
+    // a key's two lanes hold the same weight: half the sum over the lanes
+    float lw = l[a];
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) lw += __shfl_xor_sync(0xffffffffu, lw, off);
     if (lane == 0) {
       st[0] = m[a];
-      st[1] = l[a];
+      st[1] = 0.5f * lw;
+    }
+    // P V of the NG keys at a time, in their order
+    float v[8];
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      v[2 * p] = o[a][p].x;
+      v[2 * p + 1] = o[a][p].y;
     }
 #pragma unroll
-    for (int p = 0; p < C::NP; ++p) {
-      const int d2 = lane + 32 * p;
-      if (2 * d2 < DH) {
-        st[2 + 2 * d2] = o[a][p].x;
-        st[2 + 2 * d2 + 1] = o[a][p].y;
-      }
+    for (int i = 0; i < 8; ++i) {
+      float sum = v[i];
+#pragma unroll
+      for (int gi = 1; gi < C::NG; ++gi) sum += __shfl_sync(0xffffffffu, v[i], lane + gi * C::LK);
+      if (lane < C::LK) st[2 + lane * 8 + i] = sum;
     }
   }
-  __syncthreads();
+  // the states of n_states states at `from` (`stride` floats apart) of query i, dim d, merged
+  auto merge = [&](const float* from, int stride, int n_states, int d, float& mx, float& lt,
+                   float& ot) {
+    mx = -INFINITY;
+    for (int w = 0; w < n_states; ++w) mx = fmaxf(mx, from[w * stride]);
+    const float mref = mx == -INFINITY ? 0.f : mx;
+    lt = ot = 0.f;
+    for (int w = 0; w < n_states; ++w) {
+      const float f = ex2(from[w * stride] - mref);  // 0 for one that saw no key
+      lt += f * from[w * stride + 1];
+      ot += f * from[w * stride + 2 + d];
+    }
+  };
+  const int rank = c % P.nc, part = c / P.nc;
+  float* sC = sM + WARPS * MAXQ * (DH + 2);  // in the first CTA: [nc][MAXQ][DH + 2]
+  if (P.nc > 1) cluster_sync();  // the first CTA is done with its ring
+  else __syncthreads();
   for (int e = tid; e < nq * DH; e += THREADS) {
     const int i = e / DH, d = e % DH;
-    float mx = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < WARPS; ++w) mx = fmaxf(mx, sM[(w * MAXQ + i) * (DH + 2)]);
-    const float mref = mx == -INFINITY ? 0.f : mx;
-    float lt = 0.f, ot = 0.f;
-#pragma unroll
-    for (int w = 0; w < WARPS; ++w) {
-      const float* st = sM + (w * MAXQ + i) * (DH + 2);
-      const float f = ex2(st[0] - mref);  // 0 for a warp that saw no key
-      lt += f * st[1];
-      ot += f * st[2 + d];
-    }
-    const int s = stream_of(P, g, i);
-    if (P.nc == 1) {
-      out_row(P, s, b)[d] = __float2bfloat16_rn(ot * out_scale(P, s, b, lt));
-    } else {
-      float* slot = P.part + (((int64_t)s * P.B + b) * P.nc + c) * (DH + 2);
+    float mx, lt, ot;
+    merge(sM + i * (DH + 2), MAXQ * (DH + 2), WARPS, d, mx, lt, ot);
+    if (P.nc > 1) {
+      const uint32_t to = map_shared(smem_u32(sC + (rank * MAXQ + i) * (DH + 2)), 0);
       if (d == 0) {
-        slot[0] = mx;
-        slot[1] = lt;
+        st_cluster(to, mx);
+        st_cluster(to + 4, lt);
       }
-      slot[2 + d] = ot;
+      st_cluster(to + 8 + d * 4, ot);
+    } else {
+      finish_row(P, g, i, b, part, d, mx, lt, ot);
+    }
+  }
+  if (P.nc > 1) {
+    cluster_sync();  // every chunk's states have arrived
+    if (rank == 0) {
+      for (int e = tid; e < nq * DH; e += THREADS) {
+        const int i = e / DH, d = e % DH;
+        float mx, lt, ot;
+        merge(sC + i * (DH + 2), MAXQ * (DH + 2), P.nc, d, mx, lt, ot);
+        finish_row(P, g, i, b, part, d, mx, lt, ot);
+      }
     }
   }
 }
 
-// Merges the chunks' states of (stream, sequence) in chunk order.
+// Merges the clusters' states of (stream, sequence) in order.
 __global__ void __launch_bounds__(128) attn_decode_merge_kernel(const __grid_constant__ DecodeArgs P) {
   const int s = blockIdx.x, b = blockIdx.y, d = threadIdx.x;
   pdl_wait();
@@ -262,13 +346,13 @@ __global__ void __launch_bounds__(128) attn_decode_merge_kernel(const __grid_con
   int first, end;
   if (!visible(P, b, first, end)) return;
   const int row = P.d_h + 2;
-  const float* base = P.part + ((int64_t)s * P.B + b) * P.nc * row;
+  const float* base = P.part + ((int64_t)s * P.B + b) * P.np * row;
   float mx = -INFINITY;
-  for (int c = 0; c < P.nc; ++c) mx = fmaxf(mx, base[c * row]);
+  for (int c = 0; c < P.np; ++c) mx = fmaxf(mx, base[c * row]);
   const float mref = mx == -INFINITY ? 0.f : mx;
   float l = 0.f, o = 0.f;
-  for (int c = 0; c < P.nc; ++c) {
-    const float w = ex2(base[c * row] - mref);  // 0 for a chunk without keys
+  for (int c = 0; c < P.np; ++c) {
+    const float w = ex2(base[c * row] - mref);  // 0 for a cluster without keys
     l += w * base[c * row + 1];
     o += w * base[c * row + 2 + d];
   }
@@ -279,10 +363,22 @@ template <int DH, int QMAX>
 int launch_attn(const DecodeArgs& P, cudaStream_t st) {
   using C = Cfg<DH>;
   if (!set_smem_limit_once<attn_decode_kernel<DH, QMAX>>(C::SMEM)) return -1;
-  if (launch_pdl(attn_decode_kernel<DH, QMAX>, dim3(P.nc, P.G, P.B), dim3(THREADS), C::SMEM, st,
-                 P) != cudaSuccess)
-    return -1;
-  if (P.nc == 1) return 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(P.nc * P.np, P.G, P.B);
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = C::SMEM;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)P.nc;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = P.nc > 1 ? 2 : 1;
+  if (cudaLaunchKernelEx(&cfg, attn_decode_kernel<DH, QMAX>, P) != cudaSuccess) return -1;
+  if (P.np == 1) return 1;
   return launch_pdl(attn_decode_merge_kernel, dim3(P.S, P.B), dim3(DH), 0, st, P) == cudaSuccess
              ? 2
              : -1;
@@ -298,13 +394,27 @@ int launch_dh(const DecodeArgs& P, cudaStream_t st) {
 
 }  // namespace
 
-// Chunks per (sequence, KV head): enough CTAs for sixteen per SM, at least one tile each.
-int attn_decode_chunks(int B, int G, int L_max, int num_sms) {
+// Chunks of a (sequence, KV head): enough CTAs for sixteen per SM, at least a tile each. With
+// fewer pairs than SMs the latency counts: clusters of up to eight chunks, and several of them
+// only where each chunk would have more than eight tiles (one sequence of 8192 tokens: 15 us
+// against 22 with single CTAs and the second kernel). With more pairs the clusters' common
+// start costs more than the second kernel (32 sequences of 8192 tokens at d_h 128: 212 us
+// against 172).
+void attn_decode_plan(int B, int G, int L_max, int num_sms, int& nc, int& np) {
   const int64_t bg = (int64_t)B * G;
-  int64_t nc = (16 * (int64_t)num_sms + bg - 1) / bg;
   const int64_t tiles = ((int64_t)L_max + TKD - 1) / TKD;
-  if (nc > tiles) nc = tiles;
-  return nc < 1 ? 1 : (int)nc;
+  int64_t want = (16 * (int64_t)num_sms + bg - 1) / bg;
+  if (want > tiles) want = tiles;
+  if (bg >= num_sms) {
+    nc = 1;
+    np = (int)want;
+    return;
+  }
+  nc = (int)(want < kMaxCluster ? want : kMaxCluster);
+  int64_t more = (tiles + 8 * kMaxCluster - 1) / (8 * kMaxCluster);
+  const int64_t most = (want + kMaxCluster - 1) / kMaxCluster;
+  if (more > most) more = most;
+  np = (int)(more < 1 ? 1 : more);
 }
 
 int launch_attn_decode(const DecodeArgs& P, cudaStream_t st) {

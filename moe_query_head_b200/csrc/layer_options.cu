@@ -183,8 +183,8 @@ int launch_layer_decode(gqe_ctx* h, int B, int S, int has_shared, int variant, i
   P.k = h->k;
   P.d_h = d;
   P.L_max = L_max;
-  P.nc = attn_decode_chunks(B, Gl, L_max, h->num_sms);
-  while (P.nc > 1 && (int64_t)B * Gl * P.nc > kDecodeSlots) --P.nc;  // the handle's slots
+  attn_decode_plan(B, Gl, L_max, h->num_sms, P.nc, P.np);
+  while (P.np > 1 && (int64_t)B * Gl * P.np > kDecodeSlots) --P.np;  // the handle's slots
   set_decode_scores(P, o.scale, o.scores ? o.softcap : 0.f);
   const int m = launch_attn_decode(P, st);
   return m < 0 ? -1 : n + m;

@@ -314,8 +314,9 @@ int64_t gqe_attention_decode_workspace_bytes(const gqe_scores* s, int L_max) {
   const int sms = current_num_sms();
   if (sms < 0) return -1;
   if (s->B == 0) return 0;
-  const int nc = attn_decode_chunks(s->B, s->G, L_max, sms);
-  return nc > 1 ? (int64_t)s->S * s->B * nc * (s->d_h + 2) * 4 : 0;
+  int nc, np;
+  attn_decode_plan(s->B, s->G, L_max, sms, nc, np);
+  return np > 1 ? (int64_t)s->S * s->B * np * (s->d_h + 2) * 4 : 0;
 }
 
 gqe_status gqe_attention_decode(const gqe_scores* s, const gqe_heads* q,
@@ -337,10 +338,10 @@ gqe_status gqe_attention_decode(const gqe_scores* s, const gqe_heads* q,
   const int sms = current_num_sms();
   P.status = op_status_word();
   if (sms < 0 || !P.status) return GQE_ERR_CUDA;
-  P.nc = attn_decode_chunks(s->B, s->G, L_max, sms);
-  if (P.nc > 1) {
+  attn_decode_plan(s->B, s->G, L_max, sms, P.nc, P.np);
+  if (P.np > 1) {
     if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 15u)) return GQE_ERR_INVALID_ARG;
-    if (bytes < (size_t)s->S * s->B * P.nc * (d + 2) * 4) return GQE_ERR_WORKSPACE;
+    if (bytes < (size_t)s->S * s->B * P.np * (d + 2) * 4) return GQE_ERR_WORKSPACE;
     P.part = static_cast<float*>(workspace);
   }
   P.lengths = lengths;
