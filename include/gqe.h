@@ -529,7 +529,7 @@ int64_t gqe_attention_workspace_bytes(const gqe_scores* a);
 /*
  * gqe_attention_backward — gradients of gqe_attention_forward, given its inputs, out and lse, and
  * the upstream gradient dout: dq [S heads], dk and dv [G heads, summed over their streams] are
- * written (not accumulated into). `workspace`: gqe_attention_workspace_bytes bytes on the
+ * written (not accumulated into) and must not overlap the inputs. `workspace`: gqe_attention_workspace_bytes bytes on the
  * device, 16-byte aligned, used until the call's kernels end. No atomics: the result is the
  * same from run to run. The slopes and intervals get no gradient.
  */

@@ -229,9 +229,9 @@ attn_scores_kernel(const __grid_constant__ Params P) {
       if (lane == 0 && nk > 0) {
         mbar_arrive_expect_tx(q_full, C::TILE_BYTES);
         tma_load_5d(sQ, &P.tm_q, 0, qt * TQ, 0, s_idx, b_idx, q_full);
-        int st = 0;
+        int st = 0, j = 0;
         uint32_t ph = 0;
-        for (int j = 0; j < nk; ++j) {
+        for (; j < nk; ++j) {
           if (!lane_wait(&k_empty[st], ph ^ 1, P, abort_flag)) break;
           mbar_arrive_expect_tx(&k_full[st], C::TILE_BYTES);
           tma_load_5d(sK + st * C::TILE_BYTES, &P.tm_k, 0, (j0 + j) * TK, 0, kvh, b_idx,
@@ -241,13 +241,15 @@ attn_scores_kernel(const __grid_constant__ Params P) {
             ph ^= 1;
           }
         }
+        drain_ring(q_full, 1, 1);
+        drain_ring(k_full, C::K_STAGES, j);
       }
     } else if (warp == 2) {
       // -------------------------------------------------------------- V loads
       if (lane == 0) {
-        int st = 0;
+        int st = 0, j = 0;
         uint32_t ph = 0;
-        for (int j = 0; j < nk; ++j) {
+        for (; j < nk; ++j) {
           if (!lane_wait(&v_empty[st], ph ^ 1, P, abort_flag)) break;
           mbar_arrive_expect_tx(&v_full[st], C::TILE_BYTES);
           tma_load_5d(sV + st * C::V_BYTES, &P.tm_v, 0, (j0 + j) * TK, 0, kvh, b_idx,
@@ -257,6 +259,7 @@ attn_scores_kernel(const __grid_constant__ Params P) {
             ph ^= 1;
           }
         }
+        drain_ring(v_full, C::V_STAGES, j);
       }
     } else if (warp == 3) {
       // -------------------------------------------------------------- cleaning of V tiles

@@ -184,6 +184,15 @@ __device__ __forceinline__ float2 exp2_fma2_nan(float2 x) {
 
 }  // namespace tc
 
+// After a wait gave up: waits (with a limit of its own) for the `issued` tile loads of a ring that
+// are still on their way, so that none lands in shared memory the CTA has left. Where all
+// loads were consumed this returns at once.
+__device__ __forceinline__ void drain_ring(uint64_t* full, int stages, int issued) {
+  constexpr int64_t kLimit = int64_t(1) << 22;
+  for (int i = issued > stages ? issued - stages : 0; i < issued; ++i)
+    tc::mbar_wait(&full[i % stages], (uint32_t)(i / stages) & 1u, kLimit);
+}
+
 // The keys [b0, e0) that token q of sequence b sees; e0 <= b0 for a row without keys and
 // for rows past the sequence.
 struct SpanArgs {

@@ -329,9 +329,9 @@ attn_scores_dq_kernel(const __grid_constant__ Params P) {
         mbar_arrive_expect_tx(q_full, 2 * C::TILE_BYTES);
         tma_load_5d(sQ, &P.tm_q, 0, qt * TQ, 0, s_idx, b_idx, q_full);
         tma_load_5d(sdO, &P.tm_do, 0, qt * TQ, 0, s_idx, b_idx, q_full);
-        int st = 0;
+        int st = 0, j = 0;
         uint32_t ph = 0;
-        for (int j = 0; j < nk; ++j) {
+        for (; j < nk; ++j) {
           if (!lane_wait(&r_empty[st], ph ^ 1, P)) break;
           mbar_arrive_expect_tx(&r_full[st], 2 * Q::KT_BYTES);
           tma_load_5d(sK + st * Q::KT_BYTES, &P.tm_k, 0, (j0 + j) * Q::TKD, 0, kvh, b_idx,
@@ -343,6 +343,8 @@ attn_scores_dq_kernel(const __grid_constant__ Params P) {
             ph ^= 1;
           }
         }
+        drain_ring(q_full, 1, 1);
+        drain_ring(r_full, Q::STAGES, j);
       }
     } else if (warp == 3) {
       // ---------------------------------------------------------------- cleaning of K tiles
@@ -718,9 +720,9 @@ attn_scores_dkdv_kernel(const __grid_constant__ Params P) {
         mbar_arrive_expect_tx(kv_full, 2 * C::TILE_BYTES);
         tma_load_5d(sK, &P.tm_k, 0, u0, 0, g, b_idx, kv_full);
         tma_load_5d(sV, &P.tm_v, 0, u0, 0, g, b_idx, kv_full);
-        int st = 0, si = si0, r = r0;
+        int st = 0, si = si0, r = r0, j = 0;
         uint32_t ph = 0;
-        for (int j = 0; j < nj; ++j) {
+        for (; j < nj; ++j) {
           if (!lane_wait(&r_empty[st], ph ^ 1, P)) break;
           mbar_arrive_expect_tx(&r_full[st], 2 * K::QT_BYTES);
           const int s = stream_of(si), qrow = (qt0 + r) * TQJ;
@@ -735,6 +737,8 @@ attn_scores_dkdv_kernel(const __grid_constant__ Params P) {
             ph ^= 1;
           }
         }
+        drain_ring(kv_full, 1, 1);
+        drain_ring(r_full, K::STAGES, j);
       }
     } else if (warp == 3) {
       // ------------------------------------------ per job: the rows' lse, D and intervals
