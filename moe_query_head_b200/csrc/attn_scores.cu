@@ -18,6 +18,11 @@
 //              reference; P goes to TMEM in bf16 (the type of the second product), the row
 //              sums stay in 32 bits. O is rescaled in TMEM only when a row's reference moves
 //              by more than 2^8.
+// The bias of uncapped scores costs the softmax nothing: -slope (t - u) is slope c plus a number
+// of the row and the tile (c: the key's place in its tile), and slope c comes from the tensor
+// cores as sixteen more columns of the first product: (slope / scale) in three bf16 pieces on
+// the query side, (c, c, c) on the key side, exact to 24 bits. Only tiles that hold visible
+// keys behind their queries (not under a causal mask) correct the sign in registers.
 // A row's reference is -inf until it meets its first key, so rows whose first tiles are
 // masked lose nothing when their scores are far below zero.
 #include <cudaTypedefs.h>
@@ -39,7 +44,7 @@ static_assert(kSmallRegs * 128 + kLargeRegs * 128 == THREADS * (65536 / (2 * THR
 constexpr int TQ = 128, TK = 128;
 constexpr float kRescaleThreshold = 8.0f;  // log2 units
 
-template <int DH>
+template <int DH, bool BIAS>
 struct Cfg {
   // Chunk width (columns of a swizzle atom); 16-column chunks where the row sums come from
   // the tensor cores, so that the 16 columns of ones after a V tile are one chunk.
@@ -58,13 +63,18 @@ struct Cfg {
   static constexpr int V_BYTES = TILE_BYTES + ONES_BYTES;
   static constexpr int CTAS = DH <= 64 ? 2 : 1;
   static constexpr int TMEM_COLS = CTAS == 2 ? 256 : 512;
-  static constexpr int K_STAGES = DH <= 48 ? 4 : 3;
+  // With a bias its columns of the first product take the place of one K stage where shared
+  // memory is short.
+  static constexpr int AUG_BYTES = BIAS ? 2 * 128 * 32 : 0;
+  static constexpr int K_STAGES = (DH <= 48 ? 4 : 3) - (BIAS && (DH == 48 || DH == 128) ? 1 : 0);
   static constexpr int V_STAGES = DH == 64 ? 2 : 3;
-  static constexpr int SMEM = TILE_BYTES * (1 + K_STAGES) + V_STAGES * V_BYTES + 1024 + 512;
+  static constexpr int SMEM =
+      TILE_BYTES * (1 + K_STAGES) + V_STAGES * V_BYTES + AUG_BYTES + 1024 + 512;
   static constexpr int P_COL = 128, O_COL = 192;
   static_assert(O_COL + N_PV <= TMEM_COLS, "TMEM budget");
   static_assert(!SUM_MMA || CW == 16, "the ones chunk must be one 16-column chunk");
   static_assert(CTAS * (SMEM + 1024) <= 228 * 1024, "shared memory budget");
+  static_assert(SMEM <= 227 * 1024, "shared memory of a CTA");
 };
 
 // Of every 8 pairs of scores, this many take the FMA-pipe exponential and the rest MUFU's.
@@ -83,6 +93,7 @@ struct Params {
   const float* slopes;
   int T, B, S, Sr, k, nq;
   float scale_log2;  // scale log2(e), of uncapped scores
+  float inv_scale;
   CapForm cap;
   int32_t* status;
   int64_t spin;
@@ -119,17 +130,18 @@ __device__ __forceinline__ float max64(const float* s) {
   return fmaxf(fmax3(mp[0], mp[1], mp[2]), fmax3(fmax3(mp[3], mp[4], mp[5]), mp[6], mp[7]));
 }
 
-template <int DH>
-__global__ void __launch_bounds__(THREADS, Cfg<DH>::CTAS)
+template <int DH, bool BIAS>
+__global__ void __launch_bounds__(THREADS, Cfg<DH, BIAS>::CTAS)
 attn_scores_kernel(const __grid_constant__ Params P) {
-  using C = Cfg<DH>;
+  using C = Cfg<DH, BIAS>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
   uint8_t* sQ = smem;
   uint8_t* sK = smem + C::TILE_BYTES;
   uint8_t* sV = sK + C::K_STAGES * C::TILE_BYTES;
-  uint64_t* bar = reinterpret_cast<uint64_t*>(sV + C::V_STAGES * C::V_BYTES);
+  uint8_t* sAug = sV + C::V_STAGES * C::V_BYTES;  // bias columns: query side, key side
+  uint64_t* bar = reinterpret_cast<uint64_t*>(sAug + C::AUG_BYTES);
   uint64_t* q_full = bar;
   uint64_t* k_full = bar + 1;
   uint64_t* k_empty = k_full + C::K_STAGES;
@@ -190,6 +202,24 @@ attn_scores_kernel(const __grid_constant__ Params P) {
   }
   pdl_wait();  // the inputs are complete from here on
   pdl_allow_next();
+  const float slope = BIAS ? P.slopes[s_idx] : 0.f;
+  if constexpr (BIAS) {
+    // rows of 32 bytes in the 32-byte swizzle: the halves of rows 4..7 of every 8 change places
+    if (!P.cap.on) {
+      const bool keys = threadIdx.x >= 128;
+      const int rr = threadIdx.x & 127;
+      const float a = keys ? (float)rr : slope * P.inv_scale;
+      const float hi = __bfloat162float(__float2bfloat16_rn(a));
+      const float mid = keys ? a : __bfloat162float(__float2bfloat16_rn(a - hi));
+      const float lo = keys ? a : a - hi - mid;
+      uint8_t* at = sAug + (keys ? 4096 : 0) + rr * 32;
+      const int first = (rr >> 2) & 1;
+      *reinterpret_cast<uint4*>(at + first * 16) =
+          make_uint4(pack_bf16x2(hi, mid), pack_bf16x2(lo, 0.f), 0u, 0u);
+      *reinterpret_cast<uint4*>(at + (first ^ 1) * 16) = make_uint4(0u, 0u, 0u, 0u);
+      fence_async_shared();
+    }
+  }
   const int row = threadIdx.x & 127;
   const int q = qt * TQ + row;  // a softmax thread's query
   int b0 = 0, e0 = 0;
@@ -307,6 +337,10 @@ attn_scores_kernel(const __grid_constant__ Params P) {
                 (((kk * 16) / C::CW) * C::CHUNK_BYTES + ((kk * 16) % C::CW) * 2) >> 4;
             mma_ss(tmem, q_desc + o, kd + o, idesc_s, kk > 0 ? 1u : 0u);
           }
+          if constexpr (BIAS)
+            if (!P.cap.on)
+              mma_ss(tmem, smem_desc(smem_u32(sAug), 256, kSwizzle32B),
+                     smem_desc(smem_u32(sAug + 4096), 256, kSwizzle32B), idesc_s, 1u);
           mma_commit(s_full);
           mma_commit(&k_empty[kst]);
         }
@@ -361,15 +395,16 @@ attn_scores_kernel(const __grid_constant__ Params P) {
     const uint32_t t_s = tmem + lane_off;
     const uint32_t t_p = tmem + lane_off + C::P_COL;
     const uint32_t t_o = tmem + lane_off + C::O_COL;
-    const float slope2 = P.slopes ? P.slopes[s_idx] * kLog2e : 0.f;
+    const float slope2 = slope * kLog2e;
     const int q0 = qt * TQ;
     float m_used = -INFINITY, l = 0.f;
     bool ok = true;
-    by_form(P.cap.on, P.slopes != nullptr, [&](auto cap, auto bias) {
-      constexpr bool CAP = decltype(cap)::value, BIAS = decltype(bias)::value;
+    by_flag(P.cap.on, [&](auto cap) {
+      constexpr bool CAP = decltype(cap)::value;
       // a score in log2 units is (tanh of) the product times in, plus the bias
       const float in = CAP ? P.cap.log2 : P.scale_log2;
-      const float cs = BIAS ? 1.f : in;  // what is still to be multiplied after the registers' pass
+      // what is still to be multiplied after the registers' pass
+      const float cs = CAP && BIAS ? 1.f : in;
       for (int j = 0; j < nk; ++j) {
         if (!warp_wait(s_full, j & 1, P, abort_flag)) { ok = false; break; }
         tc_fence_after();
@@ -397,7 +432,7 @@ attn_scores_kernel(const __grid_constant__ Params P) {
             }
           });
         }
-        if constexpr (BIAS) {
+        if constexpr (CAP && BIAS) {
           if (kv0 + TK - 1 <= q0) {
             // every key at or before every query: the distance is linear (four chains of
             // additions, eight columns a step: packed constants would have to be moved in)
@@ -421,6 +456,15 @@ attn_scores_kernel(const __grid_constant__ Params P) {
             for (int c = 0; c < TK; ++c) s[c] = fmaf(s[c], in, -slope2 * fabsf(d0 + (float)c));
           }
         }
+        // uncapped: the products hold slope c; keys behind the query turn its sign
+        const float base = BIAS && !CAP ? (float)(kv0 - q) * slope2 : 0.f;
+        if constexpr (BIAS && !CAP) {
+          if (!P.span.causal && kv0 + TK - 1 > q0) {
+            const float d0 = (float)(kv0 - q), a2 = -2.f * slope * P.inv_scale;
+#pragma unroll
+            for (int c = 0; c < TK; ++c) s[c] = fmaf(a2, fmaxf(d0 + (float)c, 0.f), s[c]);
+          }
+        }
         if (!whole(j0 + j)) {
           const int first = b0 - kv0;
           const uint32_t count = e0 > b0 ? (uint32_t)(e0 - b0) : 0u;
@@ -437,7 +481,7 @@ attn_scores_kernel(const __grid_constant__ Params P) {
         float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
         auto half = [&](auto hc) {
           constexpr int H = decltype(hc)::value, C0 = 64 * H;
-          const float m = max64(s + C0) * cs;
+          const float m = fmaf(max64(s + C0), cs, base);
           if (m > m_used + kRescaleThreshold) {
             if constexpr (H == 1) {
               // a first half without keys holds only zeros (2^-125): the factor is then 0
@@ -454,11 +498,11 @@ attn_scores_kernel(const __grid_constant__ Params P) {
             m_used = m;
           }
           const float ref = m_used == -INFINITY ? 0.f : m_used;
-          const float2 cs2 = make_float2(cs, cs), nm2 = make_float2(-ref, -ref);
+          const float2 cs2 = make_float2(cs, cs), nm2 = make_float2(base - ref, base - ref);
 #pragma unroll
           for (int x = 0; x < 32; ++x) {
             const float2 v = make_float2(s[C0 + 2 * x], s[C0 + 2 * x + 1]);
-            const float2 t = BIAS ? add2(v, nm2) : fma2(v, cs2, nm2);
+            const float2 t = CAP && BIAS ? add2(v, nm2) : fma2(v, cs2, nm2);
             const float2 p = (x & 7) >= 8 - kFmaPairsOf8 ? exp2_fma2_nan(t)
                                                          : make_float2(ex2(t.x), ex2(t.y));
             if constexpr (!C::SUM_MMA) ls[x & 1] = add2(ls[x & 1], p);
@@ -572,10 +616,10 @@ attn_scores_kernel(const __grid_constant__ Params P) {
   }
 }
 
-template <int DH>
-int launch_dh(const AttnArgs& a, cudaStream_t st) {
-  using C = Cfg<DH>;
-  if (!set_smem_limit_once<attn_scores_kernel<DH>>(C::SMEM)) return -1;
+template <int DH, bool BIAS>
+int launch_form(const AttnArgs& a, cudaStream_t st) {
+  using C = Cfg<DH, BIAS>;
+  if (!set_smem_limit_once<attn_scores_kernel<DH, BIAS>>(C::SMEM)) return -1;
   Params P;
   memset(&P, 0, sizeof(P));
   const CUtensorMapSwizzle sw = C::CW == 64 ? CU_TENSOR_MAP_SWIZZLE_128B
@@ -605,14 +649,20 @@ int launch_dh(const AttnArgs& a, cudaStream_t st) {
   P.k = a.k;
   P.nq = (a.T + TQ - 1) / TQ;
   P.scale_log2 = a.scale * kLog2e;
+  P.inv_scale = 1.f / a.scale;
   P.cap = cap_form(a.scale, a.softcap);
   P.status = a.status;
   P.spin = a.spin > 0 ? a.spin : (int64_t)1 << 22;
   const int64_t items = (int64_t)a.B * a.S * P.nq;
-  return launch_pdl(attn_scores_kernel<DH>, dim3((unsigned)items), dim3(THREADS), C::SMEM, st,
-                    P) == cudaSuccess
+  return launch_pdl(attn_scores_kernel<DH, BIAS>, dim3((unsigned)items), dim3(THREADS), C::SMEM,
+                    st, P) == cudaSuccess
              ? 1
              : -1;
+}
+
+template <int DH>
+int launch_dh(const AttnArgs& a, cudaStream_t st) {
+  return a.slopes ? launch_form<DH, true>(a, st) : launch_form<DH, false>(a, st);
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
