@@ -249,6 +249,9 @@ attn_scores_kernel(const __grid_constant__ Params P) {
   const int full_hi = min(min(sp[3], sp[7]), min(sp[11], sp[15]));
   const int j0 = lo < hi ? lo / TK : 0;
   const int nk = lo < hi ? (hi + TK - 1) / TK - j0 : 0;  // key tiles j0 .. j0 + nk - 1
+  // The order of the key tiles: with a bias from the nearest on, since weights fall with the
+  // distance and the row references then hardly move after the first tile.
+  auto tile = [&](int j) { return BIAS ? j0 + nk - 1 - j : j0 + j; };
   auto whole = [&](int j) { return j * TK >= full_lo && (j + 1) * TK <= full_hi; };
   const int kvh = s_idx < P.Sr ? s_idx / P.k : 0;
 
@@ -264,7 +267,7 @@ attn_scores_kernel(const __grid_constant__ Params P) {
         for (; j < nk; ++j) {
           if (!lane_wait(&k_empty[st], ph ^ 1, P, abort_flag)) break;
           mbar_arrive_expect_tx(&k_full[st], C::TILE_BYTES);
-          tma_load_5d(sK + st * C::TILE_BYTES, &P.tm_k, 0, (j0 + j) * TK, 0, kvh, b_idx,
+          tma_load_5d(sK + st * C::TILE_BYTES, &P.tm_k, 0, tile(j) * TK, 0, kvh, b_idx,
                       &k_full[st]);
           if (++st == C::K_STAGES) {
             st = 0;
@@ -282,7 +285,7 @@ attn_scores_kernel(const __grid_constant__ Params P) {
         for (; j < nk; ++j) {
           if (!lane_wait(&v_empty[st], ph ^ 1, P, abort_flag)) break;
           mbar_arrive_expect_tx(&v_full[st], C::TILE_BYTES);
-          tma_load_5d(sV + st * C::V_BYTES, &P.tm_v, 0, (j0 + j) * TK, 0, kvh, b_idx,
+          tma_load_5d(sV + st * C::V_BYTES, &P.tm_v, 0, tile(j) * TK, 0, kvh, b_idx,
                       &v_full[st]);
           if (++st == C::V_STAGES) {
             st = 0;
@@ -297,7 +300,7 @@ attn_scores_kernel(const __grid_constant__ Params P) {
       uint32_t ph = 0;
       for (int j = 0; j < nk; ++j) {
         if (!warp_wait(&v_full[st], ph, P, abort_flag)) break;
-        if (!whole(j0 + j)) {
+        if (!whole(tile(j))) {
           if (clean_tile(sV + st * C::V_BYTES, C::TILE_BYTES)) {
             fence_async_shared();
             if (lane == 0) *bad_flag = 1;
@@ -360,7 +363,7 @@ attn_scores_kernel(const __grid_constant__ Params P) {
       for (int j = 0; ok && j < nk; ++j) {
         if (!warp_wait(p_ready, j & 1, P, abort_flag)) break;
         if (!warp_wait(&v_full[vst], v_phase, P, abort_flag)) break;
-        if (!whole(j0 + j)) {
+        if (!whole(tile(j))) {
           if (!warp_wait(&v_clean[vst], (clean_phase >> vst) & 1, P, abort_flag)) break;
           clean_phase ^= 1u << vst;
         }
@@ -420,7 +423,7 @@ attn_scores_kernel(const __grid_constant__ Params P) {
           __syncwarp();
           if (lane == 0) mbar_arrive(s_free);
         }
-        const int kv0 = (j0 + j) * TK;
+        const int kv0 = tile(j) * TK;
         if constexpr (CAP) {
           by_flag(!__any_sync(0xffffffffu, !(abs_max<TK>(s) < P.cap.limit)), [&](auto poly) {
 #pragma unroll
@@ -465,7 +468,7 @@ attn_scores_kernel(const __grid_constant__ Params P) {
             for (int c = 0; c < TK; ++c) s[c] = fmaf(a2, fmaxf(d0 + (float)c, 0.f), s[c]);
           }
         }
-        if (!whole(j0 + j)) {
+        if (!whole(tile(j))) {
           const int first = b0 - kv0;
           const uint32_t count = e0 > b0 ? (uint32_t)(e0 - b0) : 0u;
 #pragma unroll
