@@ -122,7 +122,8 @@ gqe_status check_scores(const gqe_scores* a, bool decode) {
   }
   const int64_t M = (int64_t)a->B * a->T;
   if (M > (int64_t(1) << 27)) return GQE_ERR_UNSUPPORTED;
-  if ((int64_t)a->B * ((a->T + 127) / 128) * a->S > INT32_MAX) return GQE_ERR_UNSUPPORTED;
+  if ((int64_t)a->B * (((int64_t)a->T + 127) / 128) * a->S > INT32_MAX)
+    return GQE_ERR_UNSUPPORTED;
   if (a->S > 65535) return GQE_ERR_UNSUPPORTED;
   return GQE_OK;
 }
@@ -278,7 +279,7 @@ gqe_status gqe_attention_forward(const gqe_scores* s, const gqe_heads* q, const 
 int64_t gqe_attention_workspace_bytes(const gqe_scores* s) {
   if (check_scores(s, false) != GQE_OK) return -1;
   const size_t dsum = align_up((size_t)s->S * s->B * s->T * 4);
-  return (int64_t)(dsum + align_up((size_t)s->B * ((s->T + 127) / 128) * 8));
+  return (int64_t)(dsum + align_up((size_t)s->B * (((size_t)s->T + 127) / 128) * 8));
 }
 
 gqe_status gqe_attention_backward(const gqe_scores* s, const gqe_heads* q, const gqe_heads* k,

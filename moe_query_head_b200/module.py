@@ -231,6 +231,9 @@ class GQEAttention(nn.Module):
         that row and y_new [B, dim] (bf16) is returned. The caller advances `lengths`.
         key_begin: [B] first visible rows of the caches (int32, on the device), or None."""
         B = x_new.shape[0]
+        if key_begin is not None and (key_begin.numel() != B or key_begin.dtype != torch.int32
+                                      or key_begin.device != x_new.device):
+            raise ValueError(f"expected {B} first rows (int32, on the device), one per sequence")
         bf = torch.bfloat16
         h = self._handle_for(B)
         w = [W.to(bf).contiguous() for W in (self.W_r, self.W_q, self.W_k, self.W_v)]

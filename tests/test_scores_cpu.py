@@ -104,7 +104,7 @@ def scores(gqe, **kw):
     (dict(S=7), INV), (dict(causal=2), INV), (dict(scale=-1.0), INV), (dict(scale=float("inf")), INV),
     (dict(softcap=-2.0), INV), (dict(softcap=float("nan")), INV), (dict(slopes=P + 2), INV),
     (dict(key_begin=P + 1), INV), (dict(key_end=P + 3), INV), (dict(d_h=72), UNS), (dict(d_h=256), UNS),
-    (dict(B=1 << 14, T=1 << 14), UNS)])
+    (dict(B=1 << 14, T=1 << 14), UNS), (dict(B=1, T=1 << 28), UNS)])
 def test_attention_refusals(G, kw, want):
     r = ctypes.byref
     a, q, k = scores(G, **kw), heads(G, 9), heads(G, 8)
@@ -258,6 +258,9 @@ def test_module_options_are_checked():
     assert {n for n, _ in m.named_parameters()} >= {"q_norm", "k_norm"}
     with pytest.raises(ValueError):
         m._ints(torch.zeros(3), 4, "cpu")
+    for bad in (torch.zeros(3, dtype=torch.int32), torch.zeros(2)):  # size, type
+        with pytest.raises(ValueError):
+            m.decode_step(torch.zeros(2, 64), None, None, None, bad)
     b, e = document_spans([2, 0, 3], 7)
     assert b.tolist() == [0, 0, 2, 2, 2, 0, 0] and e.tolist() == [2, 2, 5, 5, 5, 0, 0]
     with pytest.raises(ValueError):
