@@ -400,6 +400,7 @@ attn_scores_kernel(const __grid_constant__ Params P) {
     const uint32_t t_o = tmem + lane_off + C::O_COL;
     const float slope2 = slope * kLog2e;
     const int q0 = qt * TQ;
+    const bool live = b0 < e0;
     float m_used = -INFINITY, l = 0.f;
     bool ok = true;
     by_flag(P.cap.on, [&](auto cap) {
@@ -468,12 +469,16 @@ attn_scores_kernel(const __grid_constant__ Params P) {
             for (int c = 0; c < TK; ++c) s[c] = fmaf(a2, fmaxf(d0 + (float)c, 0.f), s[c]);
           }
         }
-        if (!whole(tile(j))) {
-          const int first = b0 - kv0;
-          const uint32_t count = e0 > b0 ? (uint32_t)(e0 - b0) : 0u;
+        // masks, each side only where some row has it inside the tile
+        if (kv0 < full_lo) {
+          const int first = live ? b0 - kv0 : TK;
 #pragma unroll
-          for (int c = 0; c < TK; ++c)
-            if ((uint32_t)(c - first) >= count) s[c] = -INFINITY;
+          for (int c = 0; c < TK; ++c) s[c] = c < first ? -INFINITY : s[c];
+        }
+        if (kv0 + TK > full_hi) {
+          const int last = live ? e0 - kv0 : 0;
+#pragma unroll
+          for (int c = 0; c < TK; ++c) s[c] = c >= last ? -INFINITY : s[c];
         }
         // Row maximum in two halves: the exponentials of the first need only its own maximum
         // and the running reference, so the second half's maximum is formed while they run. A
@@ -549,7 +554,7 @@ attn_scores_kernel(const __grid_constant__ Params P) {
     if (ok && nk > 0) ok = warp_wait(o_full, 0, P, abort_flag);
     if (ok) {
       tc_fence_after();
-      const bool valid = q < P.T, live = b0 < e0;
+      const bool valid = q < P.T;
       const int64_t tok = (int64_t)b_idx * P.T + q;
       if constexpr (C::SUM_MMA) {
         if (nk > 0) {

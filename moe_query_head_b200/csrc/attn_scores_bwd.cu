@@ -515,12 +515,16 @@ attn_scores_dq_kernel(const __grid_constant__ Params P) {
           };
           if (CAP && !poly) all(std::integral_constant<bool, false>{});
           else all(std::integral_constant<bool, true>{});
-          if (!whole(j0 + j)) {
-            const int first = b0 - kv0;
-            const uint32_t count = live ? (uint32_t)(e0 - b0) : 0u;
+          // masks, each side only where some row has it inside the step
+          if (kv0 < full_lo) {
+            const int first = live ? b0 - kv0 : 64;
 #pragma unroll
-            for (int c = 0; c < 64; ++c)
-              if ((uint32_t)(c - first) >= count) sr[c] = 0.f;
+            for (int c = 0; c < 64; ++c) sr[c] = c < first ? 0.f : sr[c];
+          }
+          if (kv0 + Q::TKD > full_hi) {
+            const int last = live ? e0 - kv0 : 0;
+#pragma unroll
+            for (int c = 0; c < 64; ++c) sr[c] = c >= last ? 0.f : sr[c];
           }
 #pragma unroll
           for (int x = 0; x < 32; ++x) pk[x] = pack_bf16x2(sr[2 * x], sr[2 * x + 1]);
