@@ -36,15 +36,14 @@ namespace {
 using tc::fma2;
 using tc::mul2;
 
-constexpr int THREADS = 256;
+constexpr int THREADS = 128;
 constexpr int WARPS = THREADS / 32;
 
 template <int DH>
 struct RowCfg {
   static constexpr int LANES = DH / 16;  // lanes that hold values
   // Lanes of a row: exactly those for 3, 5 and 6 (10, 6 and 5 rows a warp; their sums go over
-  // the row's lanes one by one), else the next power of two (the sum by halves). At head dim
-  // 48, 16384 tokens of 17 heads: 16.4 us with four lanes a row, one of them idle.
+  // the row's lanes one by one), else the next power of two (the sum by halves). 
   static constexpr bool EXACT = LANES == 3 || LANES == 5 || LANES == 6;
   static constexpr int LPR = EXACT ? LANES : LANES <= 1 ? 1 : LANES <= 2 ? 2 : LANES <= 4 ? 4 : 8;
   static constexpr int RPW = 32 / LPR;     // rows of a warp
@@ -248,8 +247,8 @@ __device__ __forceinline__ int chunk_of(const QkArgs& A, int y, int& h0, int& h1
 }
 
 // Heads whose loads are in flight per thread.
-// (32768 tokens of 17 heads of 128, two blocks an SM: forward 52.8 us at four, 59.1 at two, 53.1
-// at six; backward 87.7 at two, 95.9 at one, 100 at three. Three blocks an SM spill.)
+// (32768 tokens of 17 heads of 128, sixteen warps an SM: forward 52.8 us at four, 59.1 at two, 53.1
+// at six; backward 87.7 at two, 95.9 at one, 100 at three. More warps spill.)
 template <typename T>
 constexpr int kUnrollF = sizeof(T) == 2 ? 4 : 2;
 template <typename T>
@@ -257,7 +256,7 @@ constexpr int kUnrollB = sizeof(T) == 2 ? 2 : 1;
 
 // APPEND: one token per sequence; k and v rows go to row positions[t] of the caches.
 template <typename T, int DH, bool INTER, bool APPEND>
-__global__ void __launch_bounds__(THREADS, 2) qk_forward_kernel(const __grid_constant__ QkArgs A) {
+__global__ void __launch_bounds__(THREADS, 4) qk_forward_kernel(const __grid_constant__ QkArgs A) {
   using C = RowCfg<DH>;
   constexpr int U = kUnrollF<T>;
   pdl_wait();
@@ -356,7 +355,7 @@ __global__ void __launch_bounds__(THREADS, 2) qk_forward_kernel(const __grid_con
 
 // Blocks stride over the tokens, so that the partial weight sums stay few.
 template <typename T, int DH, bool INTER>
-__global__ void __launch_bounds__(THREADS, 2) qk_backward_kernel(const __grid_constant__ QkArgs A) {
+__global__ void __launch_bounds__(THREADS, 4) qk_backward_kernel(const __grid_constant__ QkArgs A) {
   using C = RowCfg<DH>;
   constexpr int U = kUnrollB<T>;
   __shared__ float sw[THREADS][17];
@@ -520,13 +519,13 @@ __global__ void __launch_bounds__(1024) qk_weight_sum_kernel(const __grid_consta
   }
 }
 
-// Splits the heads into chunks of equal length: as many as give the grid four blocks of eight
-// warps per SM (two of them resident), up to one per head for the smallest calls. (16384 tokens
-// of 17 heads of 48: 16.1 us at two, 16.3 at four, 17.6 at six; 5001 float32 tokens of 26 heads
-// of 64: 16.8, 15.6, 16.5.)
+// Splits the heads into chunks of equal length: as many as give the grid eight blocks per SM
+// (four of them resident), up to one per head for the smallest calls. (16384 tokens of 17 heads
+// of 48: 15.6 us at eight and at four, 17.6 at sixteen; 5001 float32 tokens of 25 heads of 64:
+// 14.9, 15.8, 16.0. Blocks of 256 threads: 16.1 and 15.9.)
 void split_heads(QkArgs& A, int64_t token_blocks, int num_sms, bool v_heads) {
   const int H = A.q.heads + A.k.heads * (v_heads ? 2 : 1);
-  int64_t want = (4 * (int64_t)num_sms + token_blocks - 1) / token_blocks;
+  int64_t want = (8 * (int64_t)num_sms + token_blocks - 1) / token_blocks;
   if (want > H) want = H;
   if (want < 1) want = 1;
   const int per = (int)((H + want - 1) / want);

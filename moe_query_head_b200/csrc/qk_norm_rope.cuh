@@ -6,7 +6,7 @@
 
 namespace gqe {
 
-// Rows of partial weight sums of a backward call at most (blocks: eight per SM).
+// Rows of partial weight sums of a backward call at most (blocks of four warps: eight per SM).
 constexpr int kQkPartialRows = 1184;
 
 struct QkTensor {
