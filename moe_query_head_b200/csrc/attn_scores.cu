@@ -49,7 +49,6 @@ struct Cfg {
   // Chunk width (columns of a swizzle atom); 16-column chunks where the row sums come from
   // the tensor cores, so that the 16 columns of ones after a V tile are one chunk.
   static constexpr int CW = (DH % 64 == 0) ? 64 : (DH % 32 == 0 && DH > 48) ? 32 : 16;
-  static constexpr int NC = DH / CW;
   static constexpr uint32_t LAYOUT =
       CW == 64 ? kSwizzle128B : (CW == 32 ? kSwizzle64B : kSwizzle32B);
   static constexpr int ROW_BYTES = CW * 2;
@@ -563,6 +562,9 @@ attn_scores_kernel(const __grid_constant__ Params P) {
           l = __uint_as_float(r[0]);
         }
       }
+      // Weights are at most 2^8 each: a larger sum is a NaN score that came through the FMA-pipe
+      // exponential, and the whole row (and its log-sum-exp) is NaN.
+      if (!(l < 1e30f)) l = __int_as_float(0x7fffffff);
       float scale = live ? 1.f / l : 0.f;
       if (valid && P.lse)
         P.lse[(int64_t)s_idx * P.B * P.T + tok] = live ? m_used + __log2f(l) : -INFINITY;

@@ -166,8 +166,8 @@ __device__ __forceinline__ void by_flag(bool flag, F&& f) {
 // 2^x of a pair on the FMA pipe, as exp2_fma.cuh's exp2_fma2 (nearest integer n of x by adding
 // and subtracting 1.5 * 2^23, then the degree-2 polynomial of 2^(x - n) fitted there, 1.9e-3,
 // the size of the bf16 rounding that follows), with NaN kept: the clamp passes a NaN on and
-// the exponent addition turns it into a value of the largest magnitudes, so that a row that
-// sees a NaN score ends as NaN instead of losing that key.
+// the exponent addition turns it into the largest float (infinity in bf16), so that a row that
+// sees a NaN score does not just lose that key; what sums such weights says NaN.
 __device__ __forceinline__ float2 exp2_fma2_nan(float2 x) {
   constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23
   asm("max.NaN.f32 %0, %0, 0fC2FA0000;" : "+f"(x.x));  // -125

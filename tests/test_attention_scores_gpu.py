@@ -226,6 +226,31 @@ def test_one_bad_value(G, bad):
     assert torch.equal(out, out2)
 
 
+@pytest.mark.parametrize("d", [48, 64, 128])
+@pytest.mark.parametrize("cap", [0.0, 20.0])
+@pytest.mark.parametrize("at", [3, 200, 333])
+def test_one_nan_key(G, d, cap, at):
+    """A NaN in one key row: every row that sees the key is NaN throughout, wherever the key lies
+    in its tile, with a log-sum-exp of NaN; rows before it keep their bits. The gradients of
+    the rows that see it are NaN."""
+    B, T = 1, 400
+    q, k, v = rows(2, T, d, 1), rows(1, T, d, 2), rows(1, T, d, 3)
+    outs = []
+    for key in (k, k.clone()):
+        if outs:
+            key[0, at, 5] = float("nan")
+        out, lse = torch.empty_like(q), torch.empty(2, T, device="cuda")
+        G.gqe_attention_forward(q, key, v, out, lse, B, T, 1, softcap=cap)
+        outs.append((out, lse))
+    (o0, l0), (o1, l1) = outs
+    assert o1[:, at:].isnan().all() and l1[:, at:].isnan().all()
+    assert torch.equal(o0[:, :at], o1[:, :at]) and torch.equal(l0[:, :at], l1[:, :at])
+    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(k)
+    k[0, at, 5] = float("nan")
+    G.gqe_attention_backward(q, k, v, o1, l1, q, dq, dk, dv, B, T, 1, softcap=cap)
+    assert dq[:, at:].isnan().all() and not dq[:, :at].isnan().any()
+
+
 def test_same_bits_streams_and_graph(G):
     """The same bits from run to run, on another stream, and from graphs replayed together."""
     B, T, Gk, k, d = 2, 300, 2, 1, 48
