@@ -5,11 +5,12 @@
 //   dq = scale dz k,  dk = scale sum over the head's streams of dz^T q,
 //   dv = sum over the head's streams of p^T dout.
 //
-// Three kernels, none with atomics (every output row is written by one CTA, so results are
+// Two kernels, none with atomics (every output row is written by one CTA, so results are
 // the same from run to run):
-//   attn_scores_d_kernel     D of every row, and the union of the intervals of every 128 rows;
-//   attn_scores_dq_kernel    CTA = (sequence, stream, 128-query tile); per 64-key step S = Q K^T
-//                            and dP into TMEM, dz in bf16 back to TMEM, dQ += dz K.
+//   attn_scores_dq_kernel    CTA = (sequence, stream, 128-query tile); D of its rows, then per
+//                            64-key step S = Q K^T and dP into TMEM, dz in bf16 back to TMEM,
+//                            dQ += dz K. It leaves D and the union of its rows' intervals for
+//                            the second kernel (a kernel of its own for them took 7 us).
 //   attn_scores_dkdv_kernel  CTA = (sequence, KV head, 128-key tile); per job (a stream of the
 //                            head, a tile of queries) S^T and dP^T, then dV += p^T dout and
 //                            dK += dz^T Q, accumulated in TMEM over all the head's streams.
@@ -55,9 +56,12 @@ struct Params {
                                         // q, dout; 128-row k, v
   SpanArgs span;
   const float* lse;
-  const float* dsum;
+  float* dsum;
+  const __nv_bfloat16* dout;  // with out: rows for D; null where dsum holds it already
+  const __nv_bfloat16* out;
+  int64_t dout_hs, dout_ts, out_hs, out_ts;
   const float* slopes;
-  const int2* blocks;
+  int2* blocks;  // [B, nq] intervals of 128 rows; null without masks
   __nv_bfloat16* dq;
   __nv_bfloat16* dk;
   __nv_bfloat16* dv;
@@ -162,66 +166,6 @@ __device__ __forceinline__ void zero_row(__nv_bfloat16* dst) {
 }
 
 // ---------------------------------------------------------------------------------------
-// D = <dout, out> of every row (blockIdx.y: stream), and of every 128 rows the union of their
-// intervals (stream 0's blocks). Lanes of a row hold 8 values each.
-// ---------------------------------------------------------------------------------------
-constexpr int D_ROWS = 128;
-template <int DH>
-__global__ void __launch_bounds__(THREADS)
-attn_scores_d_kernel(QkTensor dout, QkTensor out, float* dsum, int2* blocks, SpanArgs span, int B,
-                     int nq, int given) {
-  constexpr int LANES = DH / 8;
-  constexpr int LPR = LANES <= 2 ? 2 : LANES <= 4 ? 4 : LANES <= 8 ? 8 : 16;
-  constexpr int RPB = THREADS / LPR;
-  pdl_wait();
-  pdl_allow_next();
-  const int b = blockIdx.x / nq, qt = blockIdx.x % nq, s = blockIdx.y;
-  const int l = threadIdx.x % LPR;
-  if (!given) {
-#pragma unroll
-    for (int r0 = 0; r0 < D_ROWS; r0 += RPB) {
-      const int t = qt * D_ROWS + r0 + threadIdx.x / LPR;
-      float d = 0.f;
-      if (t < span.T && l < LANES) {
-        const int64_t tok = (int64_t)b * span.T + t;
-        const uint4 x = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(dout.data) +
-                                                        s * dout.head_stride +
-                                                        tok * dout.token_stride + 8 * l);
-        const uint4 y = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(out.data) +
-                                                        s * out.head_stride +
-                                                        tok * out.token_stride + 8 * l);
-        const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          d = fmaf(__uint_as_float(xs[i] << 16), __uint_as_float(ys[i] << 16), d);
-          d = fmaf(__uint_as_float(xs[i] & 0xffff0000u), __uint_as_float(ys[i] & 0xffff0000u), d);
-        }
-      }
-#pragma unroll
-      for (int o = LPR / 2; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
-      if (t < span.T && l == 0) dsum[(int64_t)s * B * span.T + (int64_t)b * span.T + t] = d;
-    }
-  }
-  if (!blocks || s != 0) return;
-  __shared__ int2 part[D_ROWS / 32];
-  if (threadIdx.x < D_ROWS) {
-    int b0, e0;
-    span_of(span, b, qt * D_ROWS + threadIdx.x, b0, e0);
-    const bool live = b0 < e0;
-    const int lo = __reduce_min_sync(0xffffffffu, live ? b0 : INT_MAX);
-    const int hi = __reduce_max_sync(0xffffffffu, live ? e0 : 0);
-    if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = make_int2(lo, hi);
-  }
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    int2 v = part[0];
-#pragma unroll
-    for (int i = 1; i < D_ROWS / 32; ++i) v = make_int2(min(v.x, part[i].x), max(v.y, part[i].y));
-    blocks[(int64_t)b * nq + qt] = v;
-  }
-}
-
-// ---------------------------------------------------------------------------------------
 // dQ
 // ---------------------------------------------------------------------------------------
 template <int DH>
@@ -319,6 +263,8 @@ attn_scores_dq_kernel(const __grid_constant__ Params P) {
   const int j0 = lo < hi ? lo / Q::TKD : 0;
   const int nk = lo < hi ? (hi + Q::TKD - 1) / Q::TKD - j0 : 0;  // steps j0 .. j0 + nk - 1
   auto whole = [&](int j) { return j * Q::TKD >= full_lo && (j + 1) * Q::TKD <= full_hi; };
+  if (P.blocks && s_idx == 0 && threadIdx.x == 0)
+    P.blocks[(int64_t)b_idx * P.nq + qt] = make_int2(lo, hi);
   const int kvh = s_idx < P.Sr ? s_idx / P.k : 0;
 
   if (warp < 4) {
@@ -438,7 +384,26 @@ attn_scores_dq_kernel(const __grid_constant__ Params P) {
     const int64_t tok = (int64_t)b_idx * P.T + q;
     const int64_t srow = (int64_t)s_idx * P.B * P.T + tok;
     const float lse = live ? P.lse[srow] : 0.f;
-    const float dsum = live ? P.dsum[srow] : 0.f;
+    float dsum = 0.f;
+    if (!P.dout) {
+      dsum = live ? P.dsum[srow] : 0.f;
+    } else if (valid) {
+      // D = <dout, out> in 32 bits; out is the bf16 output
+      const __nv_bfloat16* x = P.dout + (int64_t)s_idx * P.dout_hs + tok * P.dout_ts;
+      const __nv_bfloat16* y = P.out + (int64_t)s_idx * P.out_hs + tok * P.out_ts;
+#pragma unroll
+      for (int c0 = 0; c0 < DH; c0 += 8) {
+        const uint4 a = *reinterpret_cast<const uint4*>(x + c0);
+        const uint4 b = *reinterpret_cast<const uint4*>(y + c0);
+        const uint32_t as[4] = {a.x, a.y, a.z, a.w}, bs4[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          dsum = fmaf(__uint_as_float(as[i] << 16), __uint_as_float(bs4[i] << 16), dsum);
+          dsum = fmaf(__uint_as_float(as[i] & 0xffff0000u), __uint_as_float(bs4[i] & 0xffff0000u), dsum);
+        }
+      }
+      P.dsum[srow] = dsum;
+    }
     const float slope2 = P.slopes ? P.slopes[s_idx] * kLog2e : 0.f;
     const int q0 = qt * TQ;
     bool ok = true;
@@ -704,8 +669,8 @@ attn_scores_dkdv_kernel(const __grid_constant__ Params P) {
       first = min(first, sp[2 * w]);
       last = max(last, sp[2 * w + 1]);
     }
-    q_lo = last >= 0 ? first * D_ROWS : 0;
-    q_hi = last >= 0 ? min(P.T, (last + 1) * D_ROWS) : 0;
+    q_lo = last >= 0 ? first * TQ : 0;
+    q_hi = last >= 0 ? min(P.T, (last + 1) * TQ) : 0;
   }
   const int qt0 = q_lo / TQJ;
   const int per = q_lo < q_hi ? (q_hi + TQJ - 1) / TQJ - qt0 : 0;  // query tiles of a stream
@@ -1139,13 +1104,13 @@ int launch_dh(const AttnArgs& a, cudaStream_t st) {
   P.spin = a.spin > 0 ? a.spin : (int64_t)1 << 22;
   const int num_sms = current_num_sms();
   if (num_sms < 0) return -1;
-  int n = 0;
-  if (!a.dsum_given || masked) {
-    const dim3 grid((unsigned)(a.B * (int64_t)P.nq), a.dsum_given ? 1 : a.S);
-    if (launch_pdl(attn_scores_d_kernel<DH>, grid, dim3(THREADS), 0, st, a.dout, a.out, a.dsum,
-                   masked ? a.blocks : nullptr, P.span, a.B, P.nq, a.dsum_given) != cudaSuccess)
-      return -1;
-    ++n;
+  if (!a.dsum_given) {
+    P.dout = static_cast<const __nv_bfloat16*>(a.dout.data);
+    P.dout_hs = a.dout.head_stride;
+    P.dout_ts = a.dout.token_stride;
+    P.out = static_cast<const __nv_bfloat16*>(a.out.data);
+    P.out_hs = a.out.head_stride;
+    P.out_ts = a.out.token_stride;
   }
   if (!tmap_heads(&P.tm_q, a.q, a.B, a.T, DH, C::CW, TQ, sw) ||
       !tmap_heads(&P.tm_do, a.dout, a.B, a.T, DH, C::CW, TQ, sw) ||
@@ -1155,7 +1120,6 @@ int launch_dh(const AttnArgs& a, cudaStream_t st) {
   if (launch_pdl(attn_scores_dq_kernel<DH>, dim3((unsigned)((int64_t)a.B * a.S * P.nq)),
                  dim3(THREADS), Q::SMEM, st, P) != cudaSuccess)
     return -1;
-  ++n;
   if (!tmap_heads(&P.tm_q, a.q, a.B, a.T, DH, C::CW, K::TQJ, sw) ||
       !tmap_heads(&P.tm_do, a.dout, a.B, a.T, DH, C::CW, K::TQJ, sw) ||
       !tmap_heads(&P.tm_k, a.kk, a.B, a.T, DH, C::CW, TK, sw) ||
@@ -1189,7 +1153,7 @@ int launch_dh(const AttnArgs& a, cudaStream_t st) {
   cfg.attrs = attr;
   cfg.numAttrs = P.split > 1 ? 2 : 1;
   if (cudaLaunchKernelEx(&cfg, attn_scores_dkdv_kernel<DH>, P) != cudaSuccess) return -1;
-  return n + 1;
+  return 2;
 }
 
 }  // namespace
