@@ -486,7 +486,8 @@ gqe_status gqe_qk_norm_rope_append(const gqe_qk_transform* tr, int B, const gqe_
  *   G, k, S     stream s < G k reads KV head s / k; S = G k, or G k + 1 with a last stream
  *               that reads KV head 0 (the layer's shared head).
  *   scale       > 0, or 0 for 1 / sqrt(d_h).
- *   softcap     > 0, or 0 for none.
+ *   softcap     2^-13 to 2^13 (others: GQE_ERR_UNSUPPORTED, as a scale above 2^60 with a cap),
+ *               or 0 for none.
  *   slopes      [S] float32, device, or NULL for no bias.
  *   key_begin,  [B T] int32, device, positions within the sequence, or NULL for 0 and T; values
  *   key_end     outside [0, T] are cut to it. Documents packed in a sequence: the first key
@@ -529,9 +530,10 @@ int64_t gqe_attention_workspace_bytes(const gqe_scores* a);
 /*
  * gqe_attention_backward — gradients of gqe_attention_forward, given its inputs, out and lse, and
  * the upstream gradient dout: dq [S heads], dk and dv [G heads, summed over their streams] are
- * written (not accumulated into) and must not overlap the inputs. `workspace`: gqe_attention_workspace_bytes bytes on the
- * device, 16-byte aligned, used until the call's kernels end. No atomics: the result is the
- * same from run to run. The slopes and intervals get no gradient.
+ * written (not accumulated into) and must overlap nothing that the call reads. `workspace`:
+ * gqe_attention_workspace_bytes bytes on the device, 16-byte aligned, used until the call's
+ * kernels end. No atomics: the result is the same from run to run. The slopes and intervals get
+ * no gradient.
  */
 gqe_status gqe_attention_backward(const gqe_scores* a, const gqe_heads* q, const gqe_heads* k,
                                   const gqe_heads* v, const gqe_heads* out, const float* lse,

@@ -58,6 +58,13 @@ bool tmap_heads(CUtensorMap* m, const QkTensor& t, int B, int T, int d_h, int cw
 
 constexpr float kLog2e = 1.4426950408889634f;
 
+// The caps that are served. tc::tanh_from_2log2 is off by 1e-7, so a capped score by 1e-7 of the cap:
+// 8e-4 at 2^13, a fifth of a weight's bf16 half step; far larger caps would lose the score
+// itself. At the lower end and for scales below 2^60 the tanh's argument stays finite.
+inline bool cap_in_range(float scale, float softcap) {
+  return softcap == 0.f || (softcap >= 0x1p-13f && softcap <= 0x1p13f && scale <= 0x1p60f);
+}
+
 namespace tc {
 
 __device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, int c0, int c1,

@@ -399,7 +399,8 @@ attn_scores_dq_kernel(const __grid_constant__ Params P) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           dsum = fmaf(__uint_as_float(as[i] << 16), __uint_as_float(bs4[i] << 16), dsum);
-          dsum = fmaf(__uint_as_float(as[i] & 0xffff0000u), __uint_as_float(bs4[i] & 0xffff0000u), dsum);
+          dsum = fmaf(__uint_as_float(as[i] & 0xffff0000u),
+                      __uint_as_float(bs4[i] & 0xffff0000u), dsum);
         }
       }
       P.dsum[srow] = dsum;

@@ -194,6 +194,7 @@ int launch_layer_attention_backward(gqe_ctx* h, const BwdBuffers& bb, int B, int
                                     int has_shared, int causal, cudaStream_t st) {
   (void)has_shared;
   const LayerOptions& o = options(h);
+  if (!o.bwd_base) return -1;  // gqe_enable_backward could not allocate it
   const int64_t M = (int64_t)B * T;
   const int d = h->d_h, Gl = h->g1 - h->g0;
   AttnArgs a = attn_args(h, B, T, S, causal);
@@ -296,6 +297,7 @@ gqe_status gqe_set_scores(gqe_handle h, float scale, float softcap, const float*
   const void* ptrs[] = {slopes, key_begin, key_end};
   for (const void* p : ptrs)
     if (reinterpret_cast<uintptr_t>(p) & 3u) return GQE_ERR_INVALID_ARG;
+  if (!cap_in_range(scale, softcap)) return GQE_ERR_UNSUPPORTED;
   const bool on = scale > 0.f || softcap > 0.f || slopes || key_begin || key_end;
   if (on && h->dtype != GQE_BF16) return GQE_ERR_UNSUPPORTED;
   LayerOptions& o = options(h);

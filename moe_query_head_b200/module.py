@@ -43,7 +43,8 @@ class _GQEFunction(torch.autograd.Function):
         h = mod._handle_for(B * T)
         out = torch.empty((B * T, dim), dtype=bf, device=x.device)
         aux = torch.zeros(1, dtype=torch.float32, device=x.device)
-        norms = [n.detach().float().contiguous() if n is not None else None
+        # copies: the backward reads them after the caller may have changed the parameters
+        norms = [n.detach().to(torch.float32, copy=True) if n is not None else None
                  for n in (q_norm, k_norm)]
         mod._set_options(h, norms, call, x.device)
         mod._forward_call(h, xb, B, T, w, ws, wo, out, aux)
@@ -126,8 +127,16 @@ class GQEAttention(nn.Module):
         self.k_norm = nn.Parameter(torch.ones(dh)) if qk_norm else None
         self.qk_norm, self.norm_eps, self.softcap = qk_norm, norm_eps, float(softcap)
         self.rope_interleaved = rope_interleaved
+        if not self.softcap >= 0:
+            raise ValueError("softcap must be positive, or 0 for none")
+        if not norm_eps >= 0:
+            raise ValueError("norm_eps must not be negative")
+        if rope_base is None and rope_dim is not None:
+            raise ValueError("rope_dim needs a rope_base")
+        if rope_base is not None and not rope_base > 0:
+            raise ValueError("rope_base must be positive")
         rot = (rope_dim if rope_dim is not None else dh) if rope_base is not None else 0
-        if rot % 16 != 0 or rot > dh:
+        if rot % 16 != 0 or not 0 <= rot <= dh:
             raise ValueError("rope_dim must be a multiple of 16 up to head_dim")
         self._freq = [float(rope_base) ** (-2.0 * i / rot) for i in range(rot // 2)] if rot else None
         streams = self.G * self.k + bool(shared)

@@ -146,6 +146,13 @@ def test_masks(G, shape, kind):
     r.check()
 
 
+@pytest.mark.parametrize("cap", [2.0 ** -13, 2.0 ** 13])
+def test_smallest_and_largest_cap(G, cap):
+    """At the largest cap a score is off by 8e-4 (the tanh's error times the cap), a fifth of a half
+    step of its weight: inside the three that the bound of check() counts."""
+    Run(G, 1, 200, 2, 1, 1, 48, "docs", cap, False).check()
+
+
 @pytest.mark.parametrize("d", [16, 32, 48, 64, 80, 96, 112, 128])
 @pytest.mark.parametrize("cap,bias", [(0.0, False), (5.0, False), (0.0, True), (50.0, True)])
 def test_head_dims(G, d, cap, bias):

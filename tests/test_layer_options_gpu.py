@@ -155,6 +155,28 @@ def test_backward_after_another_call():
         assert torch.equal(a, b)
 
 
+def test_norm_weights_changed_before_the_backward():
+    """The backward uses the weights its forward had, as it does the projections'."""
+    wl = MAIN.with_(B=1, T=70)
+    inp = W.generate(wl)
+    o, m, call, _ = build(wl, "norm_rope")
+    load(m, inp, o)
+    x = torch.from_numpy(inp.f64("x")).float().view(1, wl.T, wl.dim).cuda()
+
+    def grads(change):
+        m.zero_grad()
+        y = m(x, **call)
+        if change:
+            with torch.no_grad():
+                for p in (m.q_norm, m.k_norm, m.W_q):
+                    p.mul_(-3.0)
+        y.float().square().sum().backward()
+        return [p.grad.clone() for p in m.parameters()]
+
+    for a, b in zip(grads(False), grads(True)):
+        assert torch.equal(a, b)
+
+
 @pytest.mark.parametrize("name", ["norm_rope", "cap", "all"])
 @pytest.mark.parametrize("variant", ["gqe", "weighted_concat"])
 def test_decode_continues_the_forward(name, variant):

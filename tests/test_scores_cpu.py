@@ -244,6 +244,30 @@ def test_layer_options_without_a_handle(G):
     assert G.lib.gqe_set_scores(None, 0.0, 1.0, None, None, None) == INV
 
 
+@pytest.mark.parametrize("kw", [dict(softcap=2.0 ** -14), dict(softcap=1e4), dict(softcap=1.0, scale=2.0 ** 61)])
+def test_caps_out_of_range(G, kw):
+    """Caps whose tanh float32 cannot give (its error is 1e-7 of the cap) are refused."""
+    r = ctypes.byref
+    a, q, k = scores(G, **kw), heads(G, 9), heads(G, 8)
+    c = heads(G, 8, ts=20 * 48, hs=2 * 20 * 48)
+    assert G.lib.gqe_attention_forward(r(a), r(q), r(k), r(k), r(q), P, None) == UNS
+    assert G.lib.gqe_attention_backward(r(a), r(q), r(k), r(k), r(q), P, r(q), r(q), r(k), r(k), P, 1 << 40,
+                                        None) == UNS
+    assert G.lib.gqe_attention_workspace_bytes(r(a)) == -1
+    q = heads(G, 9, M=2)
+    assert G.lib.gqe_attention_decode(r(a), r(q), r(c), r(c), 20, P, r(q), P, 0, None) == UNS
+    assert G.lib.gqe_attention_decode_workspace_bytes(r(a), 20) == -1
+
+
+@pytest.mark.parametrize("kw", [dict(softcap=-1.0), dict(softcap=float("nan")), dict(norm_eps=-1e-6),
+                                dict(rope_dim=32), dict(rope_base=0.0), dict(rope_base=-1e4),
+                                dict(rope_base=1e4, rope_dim=-16)])
+def test_module_option_values(kw):
+    from moe_query_head_b200.module import GQEAttention
+    with pytest.raises(ValueError):
+        GQEAttention(64, 4, 2, head_dim=32, **kw)
+
+
 def test_module_options_are_checked():
     from moe_query_head_b200.module import GQEAttention, document_spans, prefix_spans
     with pytest.raises(ValueError):
