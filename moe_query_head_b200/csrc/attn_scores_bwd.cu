@@ -5,12 +5,13 @@
 //   dq = scale dz k,  dk = scale sum over the head's streams of dz^T q,
 //   dv = sum over the head's streams of p^T dout.
 //
-// Two kernels, none with atomics (every output row is written by one CTA, so results are
+// Two kernels, none with atomics (every output value is written by one CTA, so results are
 // the same from run to run):
-//   attn_scores_dq_kernel    CTA = (sequence, stream, 128-query tile); D of its rows, then per
-//                            64-key step S = Q K^T and dP into TMEM, dz in bf16 back to TMEM,
-//                            dQ += dz K. It leaves D and the union of its rows' intervals for
-//                            the second kernel (a kernel of its own for them took 7 us).
+//   attn_scores_dq_kernel    CTA, or a cluster that shares the steps = (sequence, stream,
+//                            128-query tile); D of its rows, then per 64-key step S = Q K^T and
+//                            dP into TMEM, dz in bf16 back to TMEM, dQ += dz K. It leaves D and
+//                            the union of its rows' intervals for the second kernel (a kernel
+//                            of its own for them took 7 us).
 //   attn_scores_dkdv_kernel  CTA = (sequence, KV head, 128-key tile); per job (a stream of the
 //                            head, a tile of queries) S^T and dP^T, then dV += p^T dout and
 //                            dK += dz^T Q, accumulated in TMEM over all the head's streams.
@@ -36,7 +37,10 @@ using namespace tc;
 
 constexpr int THREADS = 256;
 constexpr int TQ = 128, TK = 128;
-constexpr int kSmallRegs = 64, kLargeRegs = 192;  // of the two warpgroups, by setmaxnreg
+// Registers of the two warpgroups, by setmaxnreg. 9 streams of 64, 5 documents in 8192 tokens, at
+// 48 / 208: 228 us, 64 / 192: 222, 80 / 176: 213; 8192 causal of 48: 442, 433, 430 (96 / 160 gains
+// on some and loses 4 % on documents of 48).
+constexpr int kSmallRegs = 80, kLargeRegs = 176;
 static_assert(kSmallRegs * 128 + kLargeRegs * 128 == THREADS * (65536 / (2 * THREADS)),
               "register split must equal the launch allocation");
 
@@ -71,7 +75,7 @@ struct Params {
   int64_t sel_stride;
   int sel_off, experts;
   int T, B, S, Sr, k, G, nq;
-  int split;  // CTAs (a cluster) that share the jobs of a key tile
+  int split;  // CTAs (a cluster) that share a query tile's steps or a key tile's jobs
   float scale, scale_log2;
   CapForm cap;
   int32_t* status;
@@ -165,6 +169,40 @@ __device__ __forceinline__ void zero_row(__nv_bfloat16* dst) {
   for (int c0 = 0; c0 < DH; c0 += 8) *reinterpret_cast<uint4*>(dst + c0) = make_uint4(0, 0, 0, 0);
 }
 
+constexpr int kMaxSplit = 4;  // CTAs of a cluster that share a tile's steps or jobs
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// The address of a shared-memory location of this CTA in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t map_shared(uint32_t addr, int rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void st_cluster_v4(uint32_t addr, const uint32_t* v) {
+  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3])
+               : "memory");
+}
+__device__ __forceinline__ void tmem_ld4_wait(uint32_t taddr, uint32_t (&r)[4]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld8_wait(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7])
+      : "r"(taddr)
+      : "memory");
+}
+
 // ---------------------------------------------------------------------------------------
 // dQ
 // ---------------------------------------------------------------------------------------
@@ -177,6 +215,9 @@ struct QCfg {
   static constexpr int SMEM = 2 * C::TILE_BYTES + STAGES * 2 * KT_BYTES + 1024 + 512;
   static constexpr int S_COL = 0, DP_COL = 64, DS_COL = 128, DQ_COL = 160;
   static_assert(DQ_COL + DH <= C::TMEM_COLS, "TMEM budget");
+  static_assert((kMaxSplit - 1) * 128 * (DH / kMaxSplit) * 4 <= 2 * C::TILE_BYTES,
+                "the Q and dO tiles' memory holds the other CTAs' parts");
+  static_assert(DH / kMaxSplit % 4 == 0, "parts of whole 16-byte stores");
   static_assert(C::CTAS * (SMEM + 1024) <= 228 * 1024, "shared memory per SM");
 };
 
@@ -206,8 +247,9 @@ attn_scores_dq_kernel(const __grid_constant__ Params P) {
   int* sp = reinterpret_cast<int*>(tmem_holder + 4);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int bs = P.B * P.S;
-  const int qt = P.nq - 1 - blockIdx.x / bs;
-  const int s_idx = blockIdx.x % bs % P.S, b_idx = blockIdx.x % bs / P.S;
+  const int item = blockIdx.x / P.split, part = blockIdx.x % P.split;  // part: rank in the cluster
+  const int qt = P.nq - 1 - item / bs;
+  const int s_idx = item % bs % P.S, b_idx = item % bs / P.S;
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
     for (int s = 0; s < Q::STAGES; ++s) {
@@ -260,12 +302,24 @@ attn_scores_dq_kernel(const __grid_constant__ Params P) {
   const int hi = max(max(sp[1], sp[5]), max(sp[9], sp[13]));
   const int full_lo = max(max(sp[2], sp[6]), max(sp[10], sp[14]));
   const int full_hi = min(min(sp[3], sp[7]), min(sp[11], sp[15]));
-  const int j0 = lo < hi ? lo / Q::TKD : 0;
-  const int nk = lo < hi ? (hi + Q::TKD - 1) / Q::TKD - j0 : 0;  // steps j0 .. j0 + nk - 1
+  // this CTA's steps j0 .. j0 + nk - 1: its share of the tile's
+  const int tile_j0 = lo < hi ? lo / Q::TKD : 0;
+  const int tile_nk = lo < hi ? (hi + Q::TKD - 1) / Q::TKD - tile_j0 : 0;
+  const int share = (tile_nk + P.split - 1) / P.split;
+  const int j0 = tile_j0 + part * share;
+  const int nk = max(0, min(share, tile_nk - part * share));
   auto whole = [&](int j) { return j * Q::TKD >= full_lo && (j + 1) * Q::TKD <= full_hi; };
-  if (P.blocks && s_idx == 0 && threadIdx.x == 0)
+  if (P.blocks && s_idx == 0 && part == 0 && threadIdx.x == 0)
     P.blocks[(int64_t)b_idx * P.nq + qt] = make_int2(lo, hi);
   const int kvh = s_idx < P.Sr ? s_idx / P.k : 0;
+  // the output row of this thread's query (softmax warps)
+  auto dq_row = [&]() -> __nv_bfloat16* {
+    const int64_t tok = (int64_t)b_idx * P.T + q;
+    if (!P.sel) return P.dq + (int64_t)s_idx * P.dq_hs + tok * P.dq_ts;
+    if (s_idx >= P.Sr) return P.dq_shared + tok * DH;
+    const int e = (s_idx / P.k) * P.experts + P.sel[tok * P.sel_stride + P.sel_off + s_idx];
+    return P.dq + tok * P.dq_ts + (int64_t)e * DH;
+  };
 
   if (warp < 4) {
     if constexpr (C::CTAS == 2) setmaxnreg_dec<kSmallRegs>();
@@ -403,7 +457,7 @@ attn_scores_dq_kernel(const __grid_constant__ Params P) {
                       __uint_as_float(bs4[i] & 0xffff0000u), dsum);
         }
       }
-      P.dsum[srow] = dsum;
+      if (part == 0) P.dsum[srow] = dsum;
     }
     const float slope2 = P.slopes ? P.slopes[s_idx] * kLog2e : 0.f;
     const int q0 = qt * TQ;
@@ -506,21 +560,58 @@ attn_scores_dq_kernel(const __grid_constant__ Params P) {
       }
     });
     if (ok && nk > 0) ok = warp_wait(acc_full, 0, P);
-    if (ok) {
-      tc_fence_after();
-      __nv_bfloat16* dst = nullptr;
-      if (valid) {
-        if (!P.sel) {
-          dst = P.dq + (int64_t)s_idx * P.dq_hs + tok * P.dq_ts;
-        } else if (s_idx < P.Sr) {
-          const int e = (s_idx / P.k) * P.experts + P.sel[tok * P.sel_stride + P.sel_off + s_idx];
-          dst = P.dq + tok * P.dq_ts + (int64_t)e * DH;
-        } else {
-          dst = P.dq_shared + tok * DH;
-        }
-      }
+    if (ok) tc_fence_after();
+    if (ok && P.split == 1) {
+      __nv_bfloat16* dst = valid ? dq_row() : nullptr;
       if (nk > 0) store_row<DH>(t_base + Q::DQ_COL, dst, P.scale, valid, !live);
       else if (valid) zero_row<DH>(dst);
+    }
+  }
+  if (P.split > 1) {
+    // The cluster's CTAs hold partial sums of the same rows. Each takes one part of the columns:
+    // it receives the others' values of them in its own shared memory (the tiles there have been
+    // read) and adds the parts in rank order.
+    cluster_sync();  // every CTA's products are done
+    const int cols = DH / P.split;  // columns of a part, a multiple of 4
+    const uint32_t t_acc = tmem + ((uint32_t)((warp & 3) * 32) << 16) + Q::DQ_COL;
+    if (warp >= 4) {
+      for (int p = 0; p < P.split; ++p) {
+        if (p == part) continue;
+        const int slot = part < p ? part : part - 1;
+        const uint32_t dst = map_shared(smem_u32(smem) + (slot * cols / 4 * 128 + row) * 16, p);
+        for (int c = 0; c < cols; c += 4) {
+          uint32_t v[4];
+          tmem_ld4_wait(t_acc + p * cols + c, v);
+          if (nk == 0) v[0] = v[1] = v[2] = v[3] = 0u;
+          st_cluster_v4(dst + c / 4 * 2048, v);
+        }
+      }
+    }
+    cluster_sync();  // all parts have arrived
+    if (warp >= 4) {
+      const bool valid = q < P.T, live = b0 < e0;
+      __nv_bfloat16* dst = valid ? dq_row() : nullptr;
+      const float4* got = reinterpret_cast<const float4*>(smem);
+      for (int c = 0; c < cols; c += 4) {
+        uint32_t v[4];
+        tmem_ld4_wait(t_acc + part * cols + c, v);
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int p = 0; p < P.split; ++p) {
+          if (p == part) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sum[i] += nk == 0 ? 0.f : __uint_as_float(v[i]);
+          } else {
+            const int slot = p < part ? p : p - 1;
+            const float4 x = got[(slot * cols + c) / 4 * 128 + row];
+            sum[0] += x.x; sum[1] += x.y; sum[2] += x.z; sum[3] += x.w;
+          }
+        }
+        if (valid)
+          *reinterpret_cast<uint2*>(dst + part * cols + c) =
+              live ? make_uint2(pack_bf16x2(sum[0] * P.scale, sum[1] * P.scale),
+                                pack_bf16x2(sum[2] * P.scale, sum[3] * P.scale))
+                   : make_uint2(0u, 0u);
+      }
     }
   }
   tc_fence_before();
@@ -536,32 +627,6 @@ attn_scores_dq_kernel(const __grid_constant__ Params P) {
 // columns of their own: at two CTAs per SM (256 columns) 48 queries for head dims up to 48
 // and 32 for 64; at one CTA per SM (512 columns) 64.
 // ---------------------------------------------------------------------------------------
-constexpr int kMaxSplit = 4;  // CTAs of a cluster that share an item's jobs
-
-__device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
-}
-// The address of a shared-memory location of this CTA in CTA `rank` of the cluster.
-__device__ __forceinline__ uint32_t map_shared(uint32_t addr, int rank) {
-  uint32_t r;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
-  return r;
-}
-__device__ __forceinline__ void st_cluster_v4(uint32_t addr, const uint32_t* v) {
-  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]),
-               "r"(v[1]), "r"(v[2]), "r"(v[3])
-               : "memory");
-}
-__device__ __forceinline__ void tmem_ld8_wait(uint32_t taddr, uint32_t (&r)[8]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7])
-      : "r"(taddr)
-      : "memory");
-}
-
 template <int DH>
 struct KCfg {
   using C = BCfg<DH>;
@@ -1061,6 +1126,26 @@ attn_scores_dkdv_kernel(const __grid_constant__ Params P) {
   }
 }
 
+// items * P.split CTAs in clusters of P.split, as a programmatic dependent launch.
+bool launch_cluster(void (*kernel)(const Params), int64_t items, int smem, cudaStream_t st,
+                    const Params& P) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(items * P.split));
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)P.split;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = P.split > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, P) == cudaSuccess;
+}
+
 template <int DH>
 int launch_dh(const AttnArgs& a, cudaStream_t st) {
   using C = BCfg<DH>;
@@ -1118,9 +1203,23 @@ int launch_dh(const AttnArgs& a, cudaStream_t st) {
       !tmap_heads(&P.tm_k, a.kk, a.B, a.T, DH, C::CW, Q::TKD, sw) ||
       !tmap_heads(&P.tm_v, a.v, a.B, a.T, DH, C::CW, Q::TKD, sw))
     return -1;
-  if (launch_pdl(attn_scores_dq_kernel<DH>, dim3((unsigned)((int64_t)a.B * a.S * P.nq)),
-                 dim3(THREADS), Q::SMEM, st, P) != cudaSuccess)
-    return -1;
+  const int64_t q_items = (int64_t)a.B * a.S * P.nq;
+  P.split = 1;
+  // A query tile's steps are split over a cluster while the grid leaves an SM's second CTA empty
+  // and every CTA keeps 16 steps of the longest row. Under a plain causal mask the last tiles have
+  // the most steps, so there also a grid below one CTA per place is split if it keeps 32. Backward
+  // of 9 streams of 48, without and with: 4096 causal tokens 175, 157 us; 2 x 2048 133, 124; 2 x
+  // 1024 55, 52. Not split, for what it would cost: 4 x 1024 causal 84, 88; all of 4096 keys 256,
+  // 263; 5 documents 106, 109. With one CTA per SM (1024 tokens of 128) it costs more: 61, 74.
+  if (C::CTAS == 2) {
+    const bool triangle = a.causal && !a.key_begin && !a.key_end;
+    auto splits = [&](int n) {
+      return (q_items * n < num_sms && a.T >= 1024 * n) ||
+             (triangle && q_items * n < 2 * (int64_t)num_sms && a.T >= 2048 * n);
+    };
+    while (P.split < kMaxSplit && splits(P.split)) P.split *= 2;
+  }
+  if (!launch_cluster(attn_scores_dq_kernel<DH>, q_items, Q::SMEM, st, P)) return -1;
   if (!tmap_heads(&P.tm_q, a.q, a.B, a.T, DH, C::CW, K::TQJ, sw) ||
       !tmap_heads(&P.tm_do, a.dout, a.B, a.T, DH, C::CW, K::TQJ, sw) ||
       !tmap_heads(&P.tm_k, a.kk, a.B, a.T, DH, C::CW, TK, sw) ||
@@ -1139,21 +1238,7 @@ int launch_dh(const AttnArgs& a, cudaStream_t st) {
   while (P.split < kMaxSplit && items * P.split < (C::CTAS == 2 ? 4 : 1) * (int64_t)num_sms &&
          jobs >= 8 * P.split)
     P.split *= 2;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(items * P.split));
-  cfg.blockDim = dim3(THREADS);
-  cfg.dynamicSmemBytes = K::SMEM;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = (unsigned)P.split;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = P.split > 1 ? 2 : 1;
-  if (cudaLaunchKernelEx(&cfg, attn_scores_dkdv_kernel<DH>, P) != cudaSuccess) return -1;
+  if (!launch_cluster(attn_scores_dkdv_kernel<DH>, items, K::SMEM, st, P)) return -1;
   return 2;
 }
 

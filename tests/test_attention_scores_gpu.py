@@ -146,6 +146,14 @@ def test_masks(G, shape, kind):
     r.check()
 
 
+@pytest.mark.parametrize("kind", ["causal", "full", "docs", "padded", "random", "nothing"])
+@pytest.mark.parametrize("T,d", [(1030, 16), (1100, 48), (2060, 64), (2050, 48)])
+def test_split_gradients(G, T, d, kind):
+    """Lengths at which two or four CTAs share a query tile's steps (and a key tile's jobs), some
+    of them with none."""
+    Run(G, 1, T, 1, 1, 1, d, kind, 0.0, False, seed=T).check()
+
+
 @pytest.mark.parametrize("cap", [2.0 ** -13, 2.0 ** 13])
 def test_smallest_and_largest_cap(G, cap):
     """At the largest cap a score is off by 8e-4 (the tanh's error times the cap), a fifth of a half
