@@ -491,7 +491,7 @@ attn_scores_kernel(const __grid_constant__ Params P) {
           const float m = fmaf(max64(s + C0), cs, base);
           if (m > m_used + kRescaleThreshold) {
             if constexpr (H == 1) {
-              // a first half without keys holds only zeros (2^-125): the factor is then 0
+              // a first half without keys holds only zeros: the factor is then 0
               const float a2 = ex2(m_used - m);
 #pragma unroll
               for (int x = 0; x < TK / 4; ++x)

@@ -172,13 +172,17 @@ __device__ __forceinline__ void by_flag(bool flag, F&& f) {
 
 // 2^x of a pair on the FMA pipe, as exp2_fma.cuh's exp2_fma2 (nearest integer n of x by adding
 // and subtracting 1.5 * 2^23, then the degree-2 polynomial of 2^(x - n) fitted there, 1.9e-3,
-// the size of the bf16 rounding that follows), with NaN kept: the clamp passes a NaN on and
-// the exponent addition turns it into the largest float (infinity in bf16), so that a row that
-// sees a NaN score does not just lose that key; what sums such weights says NaN.
+// the size of the bf16 rounding that follows), with two differences. The clamp is at -127: there
+// n is exact, the polynomial is 1 + 4.7e-4 and the exponent field becomes 0, which leaves 5e-42,
+// a zero in bf16, so a masked score (-inf) has no weight at all however large the finite value
+// beside it (below -126 what is left of a weight is denormal or nothing). And NaN is kept: the
+// clamp passes it on and the exponent addition turns it into the largest float (infinity in
+// bf16), so that a row that sees a NaN score does not just lose that key; what sums such
+// weights says NaN.
 __device__ __forceinline__ float2 exp2_fma2_nan(float2 x) {
   constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23
-  asm("max.NaN.f32 %0, %0, 0fC2FA0000;" : "+f"(x.x));  // -125
-  asm("max.NaN.f32 %0, %0, 0fC2FA0000;" : "+f"(x.y));
+  asm("max.NaN.f32 %0, %0, 0fC2FE0000;" : "+f"(x.x));  // -127
+  asm("max.NaN.f32 %0, %0, 0fC2FE0000;" : "+f"(x.y));
   const float2 j = add2(x, make_float2(kMagic, kMagic));
   const float2 n = add2(j, make_float2(-kMagic, -kMagic));
   const float2 f = fma2(n, make_float2(-1.0f, -1.0f), x);
