@@ -438,7 +438,9 @@ __global__ void __launch_bounds__(THREADS, 4) qk_backward_kernel(const __grid_co
             uy[i] = mul2(gy[i], wy[i]);
             dot = fma2(ux[i], x[i], fma2(uy[i], y[i], dot));
           }
-          const float f = rsqrtf(row_sum<DH>(ss.x + ss.y) * (1.f / DH) + A.eps);
+          // places without a token (zeros, whose factor is infinite without an epsilon) add nothing
+          const float mean = row_sum<DH>(ss.x + ss.y) * (1.f / DH);
+          const float f = on ? rsqrtf(mean + A.eps) : 0.f;
           // dx = f (w g - xh mean(w g xh)), the mean being f dot / d_h
           const float m = -f * f * (1.f / DH) * row_sum<DH>(dot.x + dot.y);
           const float2 f2 = make_float2(f, f), m2 = make_float2(m, m);
