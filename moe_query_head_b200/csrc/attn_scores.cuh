@@ -58,9 +58,10 @@ bool tmap_heads(CUtensorMap* m, const QkTensor& t, int B, int T, int d_h, int cw
 
 constexpr float kLog2e = 1.4426950408889634f;
 
-// The caps that are served. tc::tanh_from_2log2 is off by 1e-7, so a capped score by 1e-7 of the cap:
-// 8e-4 at 2^13, a fifth of a weight's bf16 half step; far larger caps would lose the score
-// itself. At the lower end and for scales below 2^60 the tanh's argument stays finite.
+// The caps that are served. tc::tanh_from_2log2 is off by 1e-7, so a capped score by 1e-7 of the
+// cap: 8e-4 at 2^13, a fifth of a weight's bf16 half step; far larger caps would lose the score
+// itself. (The polynomial below serves only scores it gives to 5e-4.) At the lower end and for
+// scales below 2^60 the tanh's argument stays finite.
 inline bool cap_in_range(float scale, float softcap) {
   return softcap == 0.f || (softcap >= 0x1p-13f && softcap <= 0x1p13f && scale <= 0x1p60f);
 }
@@ -95,14 +96,17 @@ __device__ __forceinline__ float tanh_from_2log2(float x2) {
 }
 
 // The cap's tanh of a pair of scores. An odd polynomial of degree 7 on the FMA pipe serves
-// scores up to three quarters of the cap (the ordinary case: caps are chosen above the scores);
-// a warp that meets larger ones takes the exponential and a reciprocal for its tile, 16 cycles
-// of the MUFU unit per score and warp against the polynomial's 5 of the FMA pipe. x Q(x^2)
-// was fitted for minimal largest relative error on [0, 3/4] (iteratively reweighted least
-// squares): 1.1e-5, which moves a weight by a tenth of its bf16 half step at most at a cap of
-// 50. (Degree 9 up to the cap itself: one more FMA per score, no faster where scores are
-// large.) The host folds the scores' factor into the coefficients, so the raw score is the
-// polynomial's argument.
+// scores up to three quarters of the cap (the ordinary case: caps are chosen above the scores),
+// but none above kPolyScore; a warp that meets larger ones takes the exponential and a reciprocal
+// for its tile, 16 cycles of the MUFU unit per score and warp against the polynomial's 5 of the
+// FMA pipe. x Q(x^2) was fitted for minimal largest relative error on [0, 3/4] (iteratively
+// reweighted least squares): 1.1e-5. A score of 44 is so off by 2^-11 at most, an eighth of its
+// weight's bf16 half step; tiles of a row, and the forward and its backward, may therefore
+// differ in the form they take. At a cap of 50 three quarters of the cap, 37, is the lower bound
+// of the two: 3.5e-4. (Degree 9 up to the cap itself: one more FMA per score, no faster where
+// scores are large.) The host folds the scores' factor into the coefficients, so the raw score
+// is the polynomial's argument.
+constexpr float kPolyScore = 44.f;
 struct CapForm {
   float2 c[4];   // Q's coefficients times factor^(2 i + 1), each twice
   float limit;   // largest |score| the polynomial serves
@@ -122,11 +126,12 @@ inline CapForm cap_form(float scale, float softcap) {
     power *= x * x;
   }
   f.limit = (float)(0.75 / x);
+  // beyond float32's range for the coefficients nothing is served by the polynomial
+  if (!(f.limit < 1e4f && f.limit > 1e-4f)) f.limit = 0.f;
+  f.limit = fminf(f.limit, kPolyScore / scale);
   f.t2 = (float)(x * 2.8853900817779268);
   f.log2 = softcap * 1.4426950408889634f;
   f.on = 1;
-  // beyond float32's range for the coefficients nothing is served by the polynomial
-  if (!(f.limit < 1e4f && f.limit > 1e-4f)) f.limit = 0.f;
   return f;
 }
 template <bool POLY>
