@@ -115,18 +115,29 @@ __device__ __forceinline__ bool lane_wait(uint64_t* bar, uint32_t parity, const 
   return false;
 }
 
-// Largest of 64 scores s[0..63].
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// Largest of 64 scores s[0..63]; NaN if one of them is.
 __device__ __forceinline__ float max64(const float* s) {
   float mp[8];
 #pragma unroll
-  for (int x = 0; x < 8; ++x) mp[x] = fmax3(s[x], s[8 + x], s[16 + x]);
+  for (int x = 0; x < 8; ++x) mp[x] = max3_nan(s[x], s[8 + x], s[16 + x]);
 #pragma unroll
   for (int c = 24; c < 56; c += 16)
 #pragma unroll
-    for (int x = 0; x < 8; ++x) mp[x] = fmax3(mp[x], s[c + x], s[c + 8 + x]);
+    for (int x = 0; x < 8; ++x) mp[x] = max3_nan(mp[x], s[c + x], s[c + 8 + x]);
 #pragma unroll
-  for (int x = 0; x < 8; ++x) mp[x] = fmaxf(mp[x], s[56 + x]);
-  return fmaxf(fmax3(mp[0], mp[1], mp[2]), fmax3(fmax3(mp[3], mp[4], mp[5]), mp[6], mp[7]));
+  for (int x = 0; x < 8; ++x) mp[x] = max_nan(mp[x], s[56 + x]);
+  return max_nan(max3_nan(mp[0], mp[1], mp[2]),
+                 max3_nan(max3_nan(mp[3], mp[4], mp[5]), mp[6], mp[7]));
 }
 
 template <int DH, bool BIAS>
@@ -489,7 +500,9 @@ attn_scores_kernel(const __grid_constant__ Params P) {
         auto half = [&](auto hc) {
           constexpr int H = decltype(hc)::value, C0 = 64 * H;
           const float m = fmaf(max64(s + C0), cs, base);
-          if (m > m_used + kRescaleThreshold) {
+          // A NaN score moves the reference too: the half's weights become NaN, and with them the
+          // row's sum, before a larger reference could scale a mark of it away.
+          if (!(m <= m_used + kRescaleThreshold)) {
             if constexpr (H == 1) {
               // a first half without keys holds only zeros: the factor is then 0
               const float a2 = ex2(m_used - m);
@@ -562,8 +575,9 @@ attn_scores_kernel(const __grid_constant__ Params P) {
           l = __uint_as_float(r[0]);
         }
       }
-      // Weights are at most 2^8 each: a larger sum is a NaN score that came through the FMA-pipe
-      // exponential, and the whole row (and its log-sum-exp) is NaN.
+      // Weights are at most 2^8 each: a larger sum comes from NaN weights through the FMA-pipe
+      // exponential (the largest float, infinity in bf16), and the whole row and its log-sum-exp
+      // are NaN.
       if (!(l < 1e30f)) l = __int_as_float(0x7fffffff);
       float scale = live ? 1.f / l : 0.f;
       if (valid && P.lse)
