@@ -488,7 +488,8 @@ gqe_status gqe_qk_norm_rope_append(const gqe_qk_transform* tr, int B, const gqe_
  *   scale       > 0, or 0 for 1 / sqrt(d_h).
  *   softcap     2^-13 to 2^13 (others: GQE_ERR_UNSUPPORTED, as a scale above 2^60 with a cap),
  *               or 0 for none.
- *   slopes      [S] float32, device, or NULL for no bias.
+ *   slopes      [S] float32, device, or NULL for no bias. With slopes the scale is 0 or 2^-60 to
+ *               2^60 (others: GQE_ERR_UNSUPPORTED).
  *   key_begin,  [B T] int32, device, positions within the sequence, or NULL for 0 and T; values
  *   key_end     outside [0, T] are cut to it. Documents packed in a sequence: the first key
  *               of the query's document (and its end, if not causal). A bidirectional prefix

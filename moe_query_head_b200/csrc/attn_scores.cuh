@@ -66,6 +66,12 @@ inline bool cap_in_range(float scale, float softcap) {
   return softcap == 0.f || (softcap >= 0x1p-13f && softcap <= 0x1p13f && scale <= 0x1p60f);
 }
 
+// The scales that are served with a distance bias: the uncapped forward forms slope / scale, which
+// must neither overflow nor lose its third bf16 piece.
+inline bool bias_in_range(float scale, const float* slopes) {
+  return !slopes || scale == 0.f || (scale >= 0x1p-60f && scale <= 0x1p60f);
+}
+
 namespace tc {
 
 __device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, int c0, int c1,

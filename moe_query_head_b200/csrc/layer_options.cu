@@ -297,7 +297,7 @@ gqe_status gqe_set_scores(gqe_handle h, float scale, float softcap, const float*
   const void* ptrs[] = {slopes, key_begin, key_end};
   for (const void* p : ptrs)
     if (reinterpret_cast<uintptr_t>(p) & 3u) return GQE_ERR_INVALID_ARG;
-  if (!cap_in_range(scale, softcap)) return GQE_ERR_UNSUPPORTED;
+  if (!cap_in_range(scale, softcap) || !bias_in_range(scale, slopes)) return GQE_ERR_UNSUPPORTED;
   const bool on = scale > 0.f || softcap > 0.f || slopes || key_begin || key_end;
   if (on && h->dtype != GQE_BF16) return GQE_ERR_UNSUPPORTED;
   LayerOptions& o = options(h);

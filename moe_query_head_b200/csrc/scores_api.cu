@@ -113,6 +113,7 @@ gqe_status check_scores(const gqe_scores* a, bool decode) {
   if (!(a->scale >= 0.f && a->scale < INFINITY)) return GQE_ERR_INVALID_ARG;
   if (!(a->softcap >= 0.f && a->softcap < INFINITY)) return GQE_ERR_INVALID_ARG;
   if (!cap_in_range(a->scale, a->softcap)) return GQE_ERR_UNSUPPORTED;
+  if (!bias_in_range(a->scale, a->slopes)) return GQE_ERR_UNSUPPORTED;
   const void* ptrs[] = {a->slopes, a->key_begin, decode ? nullptr : a->key_end};
   for (const void* p : ptrs)
     if (reinterpret_cast<uintptr_t>(p) & 3u) return GQE_ERR_INVALID_ARG;
