@@ -169,14 +169,39 @@ def gqe_workspace_bytes(dim, N, G, k, d_h, dtype, max_tokens) -> int:
     return int(lib.gqe_workspace_bytes(dim, N, G, k, d_h, dtype, max_tokens))
 
 
+# What has been set on each handle (by its address): its device, the number of its groups, and the
+# sizes of the slopes, positions and intervals (gqe_set_scores, gqe_set_qk_transform), which the
+# library reads without knowing them.
+_set_on = {}
+
+
+def _address(h):
+    return getattr(h, "value", h)
+
+
+def _check_sizes(h, where: str, tokens: int, k: int, shared: bool, names) -> None:
+    """The tensors set on a handle have the sizes that this call reads."""
+    on = _set_on.get(_address(h))
+    if on is None or len(on) == 2:
+        return
+    want = dict.fromkeys(names, tokens)
+    want["slopes"] = on["groups"] * k + shared
+    for name, n in want.items():
+        if on.get(name, n) != n:
+            raise GQEError(GQE_ERR_INVALID_ARG, f"{where} ({name} of {on[name]} values, {n} are read)")
+
+
 def gqe_create(dim, N, G, k, d_h, dtype, max_tokens) -> ctypes.c_void_p:
     h = ctypes.c_void_p()
     _check(lib.gqe_create(ctypes.byref(h), dim, N, G, k, d_h, dtype, max_tokens), "gqe_create")
+    _set_on[h.value] = {"device": torch.cuda.current_device(), "groups": G}
     return h
 
 
 def gqe_forward(h, x, B, T, W_r, W_q, W_k, W_v, W_shared, W_o, N, G, k, d_h, variant, causal,
                 out, aux_loss=None, stream=None) -> None:
+    _check_sizes(h, "gqe_forward", B * T, k, W_shared is not None,
+                 ("positions", "key_begin", "key_end"))
     _check(lib.gqe_forward(h, _ptr(x), B, T, _ptr(W_r), _ptr(W_q), _ptr(W_k), _ptr(W_v),
                            _ptr(W_shared), _ptr(W_o), N, G, k, d_h, variant, causal, _ptr(out),
                            _ptr(aux_loss), _stream(stream)), "gqe_forward")
@@ -186,6 +211,7 @@ def gqe_decode(h, x, B, k_cache, v_cache, L_max, lengths, W_r, W_q, W_k, W_v, W_
                N, G, k, d_h, variant, out, aux_loss=None, stream=None) -> None:
     """One generation step with a KV cache (see include/gqe.h); lengths is an int32 device
     tensor and is not modified."""
+    _check_sizes(h, "gqe_decode", B, k, W_shared is not None, ("key_begin",))
     _check(lib.gqe_decode(h, _ptr(x), B, _ptr(k_cache), _ptr(v_cache), L_max, _ptr(lengths),
                           _ptr(W_r), _ptr(W_q), _ptr(W_k), _ptr(W_v), _ptr(W_shared), _ptr(W_o),
                           N, G, k, d_h, variant, _ptr(out), _ptr(aux_loss), _stream(stream)),
@@ -195,6 +221,8 @@ def gqe_decode(h, x, B, k_cache, v_cache, L_max, lengths, W_r, W_q, W_k, W_v, W_
 def gqe_set_group_range(h, g0: int, g1: int) -> None:
     """Restricts the handle to groups g0 .. g1-1 of the layer (see include/gqe.h)."""
     _check(lib.gqe_set_group_range(h, int(g0), int(g1)), "gqe_set_group_range")
+    if _address(h) in _set_on:
+        _set_on[_address(h)]["groups"] = int(g1) - int(g0)
 
 
 def gqe_enable_backward(h) -> None:
@@ -258,6 +286,7 @@ def gqe_set_spin_limit(h, limit: int) -> None:
 
 
 def gqe_destroy(h) -> None:
+    _set_on.pop(_address(h), None)
     lib.gqe_destroy(h)
 
 
@@ -524,39 +553,64 @@ def gqe_attention_decode(q, k_cache, v_cache, lengths, out, top_k, *, scale=0.0,
           _vector(lengths, B, torch.int32, i, w), _heads(out, sq, bf, i, w), room, size)
 
 
+def _on_handle(h, sizes: dict) -> None:
+    """Notes the sizes of what has been set on a handle."""
+    on = _set_on.get(_address(h))
+    if on is not None:
+        for name, t in sizes.items():
+            if t is None:
+                on.pop(name, None)
+            else:
+                on[name] = t.numel()
+
+
+def _handle_vector(h, t, n, dtype, where: str) -> int:
+    """Address of a dense vector of n values on the handle's device; 0 for None."""
+    if t is None:
+        return 0
+    index = _device(t, where)
+    on = _set_on.get(_address(h))
+    _require(on is None or on["device"] == index, where)
+    return _vector(t, n, dtype, index, where)
+
+
 def gqe_set_qk_transform(h, d_h=0, dtype=GQE_BF16, *, norm=True, q_weight=None, k_weight=None,
                          eps=1e-6, inv_freq=None, interleaved=False, positions=None,
                          dq_weight=None, dk_weight=None) -> None:
     """Norm and rotation of the handle's queries and keys (see include/gqe.h); d_h = 0 turns
-    them off. The tensors must stay alive while calls of the handle read them."""
+    them off. The tensors must stay alive while calls of the handle read them; a gqe_forward
+    whose B T is not the size of `positions` is refused."""
     w = "gqe_set_qk_transform"
     if not d_h:
         _check(lib.gqe_set_qk_transform(h, None, None, None, None), w)
+        _on_handle(h, {"positions": None})
         return
     rot = 0 if inv_freq is None else 2 * inv_freq.numel()
 
-    def vec(t, n, dt):
-        return 0 if t is None else _vector(t, n, dt, _device(t, w), w)
+    def vec(t, n, dt=torch.float32):
+        return _handle_vector(h, t, n, dt, w)
 
-    tr = _pack_transform(d_h, dtype, int(norm), eps, vec(q_weight, d_h, torch.float32),
-                         vec(k_weight, d_h, torch.float32), rot, int(interleaved),
-                         vec(inv_freq, rot // 2, torch.float64))
+    tr = _pack_transform(d_h, dtype, int(norm), eps, vec(q_weight, d_h), vec(k_weight, d_h), rot,
+                         int(interleaved), vec(inv_freq, rot // 2, torch.float64))
     pos = 0 if positions is None else vec(positions, positions.numel(), torch.int32)
-    _check(lib.gqe_set_qk_transform(h, tr, pos, vec(dq_weight, d_h, torch.float32),
-                                    vec(dk_weight, d_h, torch.float32)), w)
+    _check(lib.gqe_set_qk_transform(h, tr, pos, vec(dq_weight, d_h), vec(dk_weight, d_h)), w)
+    _on_handle(h, {"positions": positions})
 
 
 def gqe_set_scores(h, *, scale=0.0, softcap=0.0, slopes=None, key_begin=None,
                    key_end=None) -> None:
     """Cap, bias and intervals of the handle's scores (see include/gqe.h); without arguments they
-    are off. The tensors must stay alive while calls of the handle read them."""
+    are off. The tensors must stay alive while calls of the handle read them; a gqe_forward
+    (B T) or gqe_decode (B) that would read another number of values than they hold is
+    refused."""
     w = "gqe_set_scores"
 
     def vec(t, dt):
-        return 0 if t is None else _vector(t, t.numel(), dt, _device(t, w), w)
+        return 0 if t is None else _handle_vector(h, t, t.numel(), dt, w)
 
     _check(lib.gqe_set_scores(h, scale, softcap, vec(slopes, torch.float32),
                               vec(key_begin, torch.int32), vec(key_end, torch.int32)), w)
+    _on_handle(h, {"slopes": slopes, "key_begin": key_begin, "key_end": key_end})
 
 
 def gqe_check_op_status(stream=None, device=None) -> int:
