@@ -603,8 +603,9 @@ gqe_status gqe_set_scores(gqe_handle h, float scale, float softcap, const float*
 /*
  * gqe_check_op_status — synchronise `stream`, then read and clear the current device's status
  * word of the operators above: GQE_OK, GQE_ERR_TIMEOUT (a wait gave up: outputs since the last
- * check are invalid) or GQE_ERR_INVALID_ARG (a position outside its cache). Not while a stream
- * is being captured.
+ * check are invalid) or GQE_ERR_INVALID_ARG (a position outside its cache). The word is one per
+ * device, for every stream and thread: who checks first sees the report of any of them (a
+ * timeout before a position). Not while a stream is being captured.
  */
 gqe_status gqe_check_op_status(void* stream);
 

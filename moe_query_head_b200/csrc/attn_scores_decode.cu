@@ -129,7 +129,7 @@ attn_decode_kernel(const __grid_constant__ DecodeArgs P) {
   pdl_allow_next();
   int first, end;
   if (!visible(P, b, first, end)) {
-    if (tid == 0 && c == 0 && g == 0) atomicExch(P.status, kStatusBadInput);
+    if (tid == 0 && c == 0 && g == 0) atomicCAS(P.status, kStatusOk, kStatusBadInput);
     return;
   }
   const int nq = P.k + (g == 0 && P.S > P.G * P.k ? 1 : 0);

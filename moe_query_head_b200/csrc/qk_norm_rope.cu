@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(THREADS, 4) qk_forward_kernel(const __grid_con
   if constexpr (APPEND) {
     // -1: an idle slot; other positions outside the cache are reported. Nothing is written.
     if (t < A.M && (pos < 0 || pos >= A.L_max)) {
-      if ((pos != -1 || !A.idle_ok) && l == 0) atomicExch(A.status, kStatusBadInput);
+      if ((pos != -1 || !A.idle_ok) && l == 0) atomicCAS(A.status, kStatusOk, kStatusBadInput);
       on = false;
     }
   }

@@ -16,6 +16,9 @@ namespace gqe {
 __device__ int32_t g_op_status;
 
 namespace {
+// Clears the word if it still holds what was read: a report that came in between stays.
+__global__ void clear_status_kernel(int32_t* word, int32_t seen) { atomicCAS(word, seen, 0); }
+
 constexpr int kMaxDevices = 64;
 std::atomic<int32_t*> g_status_words[kMaxDevices];  // looked up once per device
 std::atomic<int> g_num_sms[kMaxDevices];
@@ -367,7 +370,9 @@ gqe_status gqe_check_op_status(void* stream) {
   int32_t v = 0;
   if (cudaMemcpy(&v, word, 4, cudaMemcpyDeviceToHost) != cudaSuccess) return GQE_ERR_CUDA;
   if (v == kStatusOk) return GQE_OK;
-  if (cudaMemset(word, 0, 4) != cudaSuccess) return GQE_ERR_CUDA;
+  clear_status_kernel<<<1, 1, 0, st>>>(word, v);
+  if (cudaGetLastError() != cudaSuccess || cudaStreamSynchronize(st) != cudaSuccess)
+    return GQE_ERR_CUDA;
   return v == kStatusBadInput ? GQE_ERR_INVALID_ARG : GQE_ERR_TIMEOUT;
 }
 
