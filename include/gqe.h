@@ -481,7 +481,8 @@ gqe_status gqe_qk_norm_rope_append(const gqe_qk_transform* tr, int B, const gqe_
  *     z = scale <q_t, k_u>;  z = softcap tanh(z / softcap);  z -= slopes[s] |t - u|
  * and its weights the softmax of z over those keys. A row that sees no key gives zeros and has
  * no gradient. What is masked may hold anything: infinities and NaN in keys and values reach
- * only the rows that see them (as NaN).
+ * only the rows that see them (as NaN; in the forward a score of -infinity beside finite ones is
+ * a weight of zero).
  *   B, T        sequences and tokens of each; tokens are sequence-major (b T + t).
  *   G, k, S     stream s < G k reads KV head s / k; S = G k, or G k + 1 with a last stream
  *               that reads KV head 0 (the layer's shared head).

@@ -64,6 +64,8 @@ struct Params {
   const __nv_bfloat16* dout;  // with out: rows for D; null where dsum holds it already
   const __nv_bfloat16* out;
   int64_t dout_hs, dout_ts, out_hs, out_ts;
+  const __nv_bfloat16* keys;  // for the rare rows that see an infinity or NaN
+  int64_t key_hs, key_ts;
   const float* slopes;
   int2* blocks;  // [B, nq] intervals of 128 rows; null without masks
   __nv_bfloat16* dq;
@@ -143,6 +145,16 @@ __device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t* r) {
 // where the cap's polynomial keeps the FMA pipe busy.
 template <bool CAP, bool BIAS>
 constexpr int kBwdFma = CAP ? 0 : 2;
+
+// A product that takes denormals for zeros: what the FMA-pipe exponential leaves of a score of
+// -infinity (5e-42) is then no factor of dz.
+__device__ __forceinline__ float2 mul2_ftz(float2 a, float2 b) {
+  uint64_t d;
+  asm("mul.rn.ftz.f32x2 %0, %1, %2;"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<uint64_t*>(&a)), "l"(*reinterpret_cast<uint64_t*>(&b)));
+  return *reinterpret_cast<float2*>(&d);
+}
 
 // Writes a TMEM accumulator row (DH columns, scaled) as bf16.
 template <int DH>
@@ -244,6 +256,7 @@ attn_scores_dq_kernel(const __grid_constant__ Params P) {
   uint64_t* d_free = d_ready + 1;
   uint64_t* acc_full = d_free + 1;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(acc_full + 1);
+  volatile int* bad_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   int* sp = reinterpret_cast<int*>(tmem_holder + 4);
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int bs = P.B * P.S;
@@ -262,6 +275,7 @@ attn_scores_dq_kernel(const __grid_constant__ Params P) {
     mbar_init(d_ready, 4);
     mbar_init(d_free, 1);
     mbar_init(acc_full, 1);
+    *bad_flag = 0;
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -321,6 +335,7 @@ attn_scores_dq_kernel(const __grid_constant__ Params P) {
     return P.dq + tok * P.dq_ts + (int64_t)e * DH;
   };
 
+  bool nan_row = false;
   if (warp < 4) {
     if constexpr (C::CTAS == 2) setmaxnreg_dec<kSmallRegs>();
     if (warp == 0) {
@@ -353,7 +368,11 @@ attn_scores_dq_kernel(const __grid_constant__ Params P) {
       for (int j = 0; j < nk; ++j) {
         if (!warp_wait(&r_full[st], ph, P)) break;
         if (!whole(j0 + j)) {
-          if (clean_tile(sK + st * Q::KT_BYTES, Q::KT_BYTES)) fence_async_shared();
+          if (clean_tile(sK + st * Q::KT_BYTES, Q::KT_BYTES)) {
+            fence_async_shared();
+            if (lane == 0) *bad_flag = 1;
+            __threadfence_block();
+          }
           __syncwarp();
           if (lane == 0) mbar_arrive(&r_clean[st]);
         }
@@ -501,7 +520,7 @@ attn_scores_dq_kernel(const __grid_constant__ Params P) {
             if constexpr (CAP)  // (1 - tanh^2) (dP - D) = (tanh^2 - 1) (D - dP)
               return mul2(mul2(p, fma2(dp, m1, nD2)), fma2(v, v, m1));
             else
-              return mul2(p, add2(dp, nD2));
+              return mul2_ftz(p, add2(dp, nD2));
           };
           const float d0 = (float)(kv0 - q);
           auto all = [&](auto pl) {
@@ -561,9 +580,25 @@ attn_scores_dq_kernel(const __grid_constant__ Params P) {
     });
     if (ok && nk > 0) ok = warp_wait(acc_full, 0, P);
     if (ok) tc_fence_after();
+    // A cleaned K tile hides the infinities and NaN that a row does see, and its scores of -inf
+    // were formed without them: the row becomes NaN (rare; whole tiles are not cleaned and carry
+    // theirs themselves).
+    if (ok && nk > 0 && *bad_flag && valid && live) {
+      for (int j = j0; j < j0 + nk; ++j) {
+        if (whole(j)) continue;
+        const int u1 = min(e0, (j + 1) * Q::TKD);
+        for (int u = max(b0, j * Q::TKD); u < u1; ++u) {
+          const uint32_t* kr = reinterpret_cast<const uint32_t*>(
+              P.keys + (int64_t)kvh * P.key_hs + ((int64_t)b_idx * P.T + u) * P.key_ts);
+          for (int c = 0; c < DH / 2; ++c)
+            if ((kr[c] & 0x7f80u) == 0x7f80u || (kr[c] & 0x7f800000u) == 0x7f800000u) nan_row = true;
+        }
+      }
+    }
     if (ok && P.split == 1) {
       __nv_bfloat16* dst = valid ? dq_row() : nullptr;
-      if (nk > 0) store_row<DH>(t_base + Q::DQ_COL, dst, P.scale, valid, !live);
+      const float sc = nan_row ? __int_as_float(0x7fffffff) : P.scale;
+      if (nk > 0) store_row<DH>(t_base + Q::DQ_COL, dst, sc, valid, !live);
       else if (valid) zero_row<DH>(dst);
     }
   }
@@ -583,6 +618,7 @@ attn_scores_dq_kernel(const __grid_constant__ Params P) {
           uint32_t v[4];
           tmem_ld4_wait(t_acc + p * cols + c, v);
           if (nk == 0) v[0] = v[1] = v[2] = v[3] = 0u;
+          if (nan_row) v[0] = v[1] = v[2] = v[3] = 0x7fffffffu;
           st_cluster_v4(dst + c / 4 * 2048, v);
         }
       }
@@ -599,7 +635,8 @@ attn_scores_dq_kernel(const __grid_constant__ Params P) {
         for (int p = 0; p < P.split; ++p) {
           if (p == part) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) sum[i] += nk == 0 ? 0.f : __uint_as_float(v[i]);
+            for (int i = 0; i < 4; ++i)
+              sum[i] += nan_row ? __int_as_float(0x7fffffff) : nk == 0 ? 0.f : __uint_as_float(v[i]);
           } else {
             const int slot = p < part ? p : p - 1;
             const float4 x = got[(slot * cols + c) / 4 * 128 + row];
@@ -1001,7 +1038,7 @@ attn_scores_dkdv_kernel(const __grid_constant__ Params P) {
                 d[h] = mul2(mul2(g, mul2(p[h], make_float2(-1.f, -1.f))),
                             fma2(v, v, make_float2(-1.f, -1.f)));
               else
-                d[h] = mul2(p[h], g);
+                d[h] = mul2_ftz(p[h], g);
             }
             if constexpr (!PLAIN) {
               const int4 B4 = reinterpret_cast<const int4*>(sB)[x4];
@@ -1181,6 +1218,9 @@ int launch_dh(const AttnArgs& a, cudaStream_t st) {
   P.S = a.S;
   P.Sr = a.G * a.k;
   P.k = a.k;
+  P.keys = static_cast<const __nv_bfloat16*>(a.kk.data);
+  P.key_hs = a.kk.head_stride;
+  P.key_ts = a.kk.token_stride;
   P.G = a.G;
   P.nq = (a.T + TQ - 1) / TQ;
   P.scale = a.scale;
