@@ -575,10 +575,11 @@ attn_scores_kernel(const __grid_constant__ Params P) {
           l = __uint_as_float(r[0]);
         }
       }
-      // Weights are at most 2^8 each: a larger sum comes from NaN weights through the FMA-pipe
-      // exponential (the largest float, infinity in bf16), and the whole row and its log-sum-exp
-      // are NaN.
-      if (!(l < 1e30f)) l = __int_as_float(0x7fffffff);
+      // The largest score's weight is near 1 (as near as its float32 is to the reference) and none
+      // is far above 2^8. A sum of 1e30 comes from NaN weights through the FMA-pipe exponential
+      // (the largest float, infinity in bf16), one below 1e-30 from scores that are all -infinity
+      // (5e-42 each): the whole row and its log-sum-exp are NaN.
+      if (!(l > 1e-30f && l < 1e30f)) l = __int_as_float(0x7fffffff);
       float scale = live ? 1.f / l : 0.f;
       if (valid && P.lse)
         P.lse[(int64_t)s_idx * P.B * P.T + tok] = live ? m_used + __log2f(l) : -INFINITY;

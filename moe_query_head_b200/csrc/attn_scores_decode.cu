@@ -69,8 +69,10 @@ __device__ __forceinline__ __nv_bfloat16* out_row(const DecodeArgs& P, int s, in
   const int64_t head = s == P.S - 1 && P.last_off >= 0 ? P.last_off : (int64_t)s * P.out.head_stride;
   return static_cast<__nv_bfloat16*>(P.out.data) + head + (int64_t)b * P.out.token_stride;
 }
-__device__ __forceinline__ float out_scale(const DecodeArgs& P, int s, int b, float l) {
-  float sc = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // no key: zeros; NaN stays
+// The factor of a row with the sum l: 0 without keys (`any`). With keys whose scores are all
+// -infinity l and O are 0, which gives NaN.
+__device__ __forceinline__ float out_scale(const DecodeArgs& P, int s, int b, float l, bool any) {
+  float sc = any ? 1.f / l : 0.f;
   if (P.psel && s < P.G * P.k) sc *= P.psel[(int64_t)b * P.psel_stride + P.psel_off + s];
   return sc;
 }
@@ -84,10 +86,10 @@ __device__ __forceinline__ bool visible(const DecodeArgs& P, int b, int& first, 
 
 // (m, l, O[d]) of query i over the keys of one cluster: the output, or the cluster's state.
 __device__ __forceinline__ void finish_row(const DecodeArgs& P, int g, int i, int b, int part, int d,
-                                           float mx, float lt, float ot) {
+                                           float mx, float lt, float ot, bool any) {
   const int s = stream_of(P, g, i);
   if (P.np == 1) {
-    out_row(P, s, b)[d] = __float2bfloat16_rn(ot * out_scale(P, s, b, lt));
+    out_row(P, s, b)[d] = __float2bfloat16_rn(ot * out_scale(P, s, b, lt, any));
     return;
   }
   float* slot = P.part + (((int64_t)s * P.B + b) * P.np + part) * (P.d_h + 2);
@@ -322,7 +324,7 @@ attn_decode_kernel(const __grid_constant__ DecodeArgs P) {
       }
       st_cluster(to + 8 + d * 4, ot);
     } else {
-      finish_row(P, g, i, b, part, d, mx, lt, ot);
+      finish_row(P, g, i, b, part, d, mx, lt, ot, n > 0);
     }
   }
   if (P.nc > 1) {
@@ -332,7 +334,7 @@ attn_decode_kernel(const __grid_constant__ DecodeArgs P) {
         const int i = e / DH, d = e % DH;
         float mx, lt, ot;
         merge(sC + i * (DH + 2), MAXQ * (DH + 2), P.nc, d, mx, lt, ot);
-        finish_row(P, g, i, b, part, d, mx, lt, ot);
+        finish_row(P, g, i, b, part, d, mx, lt, ot, n > 0);
       }
     }
   }
@@ -356,7 +358,7 @@ __global__ void __launch_bounds__(128) attn_decode_merge_kernel(const __grid_con
     l += w * base[c * row + 1];
     o += w * base[c * row + 2 + d];
   }
-  out_row(P, s, b)[d] = __float2bfloat16_rn(o * out_scale(P, s, b, l));
+  out_row(P, s, b)[d] = __float2bfloat16_rn(o * out_scale(P, s, b, l, first < end));
 }
 
 template <int DH, int QMAX>
