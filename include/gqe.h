@@ -443,7 +443,7 @@ int64_t gqe_qk_norm_rope_workspace_bytes(int d_h);
  *   dq_out, dk_out upstream gradients of its outputs.
  *   dq, dk         written: gradients of q and k (may be dq_out and dk_out themselves).
  *   dq_weight,     [d_h] float32, device, written (not accumulated into): gradients of the
- *   dk_weight      weights, zeros without a norm; NULL: not wanted.
+ *   dk_weight      weights, zeros without a norm; NULL: not wanted. Not the same buffer.
  *   workspace      gqe_qk_norm_rope_workspace_bytes bytes on the device, 16-byte aligned, where
  *                  a weight gradient is wanted (NULL otherwise). Used until the call's kernels
  *                  end: calls that may run at the same time need one each.
@@ -576,7 +576,7 @@ gqe_status gqe_attention_decode(const gqe_scores* a, const gqe_heads* q,
  *               position within the sequence.
  *   dq_weight,  [d_h] float32, device: gqe_backward (gqe_backward_begin) writes the weights'
  *   dk_weight   gradients there; a handle restricted to a group range writes its share. NULL:
- *               not wanted. They may be set anew between a forward and its backward.
+ *               not wanted. Not the same buffer. They may be set anew between a forward and its backward.
  * gqe_get_tensor's Q and K stay the projections of bf16 handles. Allocates (cudaMalloc) a second
  * buffer of queries and keys at the first call, and their gradients' where the backward pass
  * is enabled; not while a stream is being captured.

@@ -269,6 +269,7 @@ gqe_status gqe_set_qk_transform(gqe_handle h, const gqe_qk_transform* tr,
   const void* ptrs[] = {positions, dq_weight, dk_weight};
   for (const void* p : ptrs)
     if (reinterpret_cast<uintptr_t>(p) & 3u) return GQE_ERR_INVALID_ARG;
+  if (dq_weight && dq_weight == dk_weight) return GQE_ERR_INVALID_ARG;  // two sums, one place
   const gqe_qk_transform& t = o.tr;
   const bool same = o.transform && t.norm == tr->norm && t.eps == tr->eps &&
                     t.q_weight == tr->q_weight && t.k_weight == tr->k_weight &&

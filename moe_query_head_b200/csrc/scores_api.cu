@@ -200,6 +200,7 @@ gqe_status gqe_qk_norm_rope_backward(const gqe_qk_transform* tr, int M, const gq
     return GQE_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(dq_weight) & 3u) || (reinterpret_cast<uintptr_t>(dk_weight) & 3u))
     return GQE_ERR_INVALID_ARG;
+  if (dq_weight && dq_weight == dk_weight) return GQE_ERR_INVALID_ARG;  // two sums, one place
   const int esz = tr->dtype == GQE_F32 ? 4 : 2, d = tr->d_h;
   QkArgs A = transform_args(*tr);
   if (!take(q, q->heads, M, d, esz, d, A.q) || !take(k, k->heads, M, d, esz, d, A.k) ||
