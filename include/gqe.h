@@ -577,7 +577,10 @@ gqe_status gqe_attention_decode(const gqe_scores* a, const gqe_heads* q,
  *   dq_weight,  [d_h] float32, device: gqe_backward (gqe_backward_begin) writes the weights'
  *   dk_weight   gradients there; a handle restricted to a group range writes its share. NULL:
  *               not wanted. Not the same buffer. They may be set anew between a forward and its backward.
- * gqe_get_tensor's Q and K stay the projections of bf16 handles. Allocates (cudaMalloc) a second
+ * gqe_get_tensor's Q and K stay the projections of bf16 handles. A cache is filled from a forward
+ * by gqe_qk_norm_rope of that K, with no query heads and the forward's transform and positions,
+ * and from its V as it is; gqe_decode goes on from there where token t of a sequence is its
+ * cache's row t at position t (it takes no other positions). Allocates (cudaMalloc) a second
  * buffer of queries and keys at the first call, and their gradients' where the backward pass
  * is enabled; not while a stream is being captured.
  */

@@ -238,7 +238,9 @@ class GQEAttention(nn.Module):
         """One generation step (gqe_decode): x_new [B, dim], one new token per sequence at
         position lengths[b] (int32, on the device); its K / V are written into the caches at
         that row and y_new [B, dim] (bf16) is returned. The caller advances `lengths`.
-        key_begin: [B] first visible rows of the caches (int32, on the device), or None."""
+        key_begin: [B] first visible rows of the caches (int32, on the device), or None. A
+        rotated key has its row as its position: a forward with `positions` of its own is not
+        continued."""
         B = x_new.shape[0]
         if key_begin is not None and (key_begin.numel() != B or key_begin.dtype != torch.int32
                                       or key_begin.device != x_new.device):
