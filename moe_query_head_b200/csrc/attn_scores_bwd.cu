@@ -524,33 +524,33 @@ attn_scores_dq_kernel(const __grid_constant__ Params P) {
           };
           const float d0 = (float)(kv0 - q);
           auto all = [&](auto pl) {
-          if (!BIAS || kv0 + Q::TKD - 1 <= q0) {
-            // no bias, or every key at or before every query: the distance is linear (four
-            // chains of additions, eight columns a step: packed constants would be moved in)
-            const float base = fmaf(d0, slope2, -lse);
-            const float2 step = make_float2(8.f * slope2, 8.f * slope2);
-            float2 chain[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              chain[i] = make_float2(fmaf(slope2, (float)(2 * i), base),
-                                     fmaf(slope2, (float)(2 * i + 1), base));
-#pragma unroll
-            for (int x = 0; x < 32; ++x) {
-              const float2 d = pair(x, BIAS ? chain[x & 3] : nl2, pl);
-              if constexpr (BIAS) chain[x & 3] = add2(chain[x & 3], step);
-              sr[2 * x] = d.x;
-              sr[2 * x + 1] = d.y;
+            if (!BIAS || kv0 + Q::TKD - 1 <= q0) {
+              // no bias, or every key at or before every query: the distance is linear (four
+              // chains of additions, eight columns a step: packed constants would be moved in)
+              const float base = fmaf(d0, slope2, -lse);
+              const float2 step = make_float2(8.f * slope2, 8.f * slope2);
+              float2 chain[4];
+  #pragma unroll
+              for (int i = 0; i < 4; ++i)
+                chain[i] = make_float2(fmaf(slope2, (float)(2 * i), base),
+                                       fmaf(slope2, (float)(2 * i + 1), base));
+  #pragma unroll
+              for (int x = 0; x < 32; ++x) {
+                const float2 d = pair(x, BIAS ? chain[x & 3] : nl2, pl);
+                if constexpr (BIAS) chain[x & 3] = add2(chain[x & 3], step);
+                sr[2 * x] = d.x;
+                sr[2 * x + 1] = d.y;
+              }
+            } else {
+  #pragma unroll
+              for (int x = 0; x < 32; ++x) {
+                const float2 d =
+                    pair(x, make_float2(fmaf(-slope2, fabsf(d0 + (float)(2 * x)), -lse),
+                                        fmaf(-slope2, fabsf(d0 + (float)(2 * x + 1)), -lse)), pl);
+                sr[2 * x] = d.x;
+                sr[2 * x + 1] = d.y;
+              }
             }
-          } else {
-#pragma unroll
-            for (int x = 0; x < 32; ++x) {
-              const float2 d =
-                  pair(x, make_float2(fmaf(-slope2, fabsf(d0 + (float)(2 * x)), -lse),
-                                      fmaf(-slope2, fabsf(d0 + (float)(2 * x + 1)), -lse)), pl);
-              sr[2 * x] = d.x;
-              sr[2 * x + 1] = d.y;
-            }
-          }
           };
           if (CAP && !poly) all(std::integral_constant<bool, false>{});
           else all(std::integral_constant<bool, true>{});
@@ -1006,60 +1006,60 @@ attn_scores_dkdv_kernel(const __grid_constant__ Params P) {
           for (int i = 0; i < 4; ++i)
             chain[i] = make_float2(-slope2 * (d0 + (float)(2 * i)), -slope2 * (d0 + (float)(2 * i + 1)));
           auto all = [&](auto pl, auto pn) {
-          constexpr bool PLAIN = decltype(pn)::value;
-#pragma unroll
-          for (int x4 = 0; x4 < TQJ / 4; ++x4) {
-            const float4 L4 = reinterpret_cast<const float4*>(sL)[x4];  // -lse
-            const float4 D4 = reinterpret_cast<const float4*>(sD)[x4];  // -D
-            const float2 nL[2] = {make_float2(L4.x, L4.y), make_float2(L4.z, L4.w)};
-            const float2 nD[2] = {make_float2(D4.x, D4.y), make_float2(D4.z, D4.w)};
-            float2 p[2], d[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int c = 4 * x4 + 2 * h;
-              float2 v = make_float2(sr[c], sr[c + 1]);
-              if constexpr (CAP) v = cap_tanh<decltype(pl)::value>(P.cap, v);
-              float2 b = nL[h];
-              if constexpr (BIAS) {
-                if constexpr (PLAIN) {
-                  b = add2(b, chain[(c >> 1) & 3]);
-                  chain[(c >> 1) & 3] = add2(chain[(c >> 1) & 3], step);
-                } else {
-                  b.x = fmaf(-slope2, fabsf(d0 + (float)c), b.x);
-                  b.y = fmaf(-slope2, fabsf(d0 + (float)(c + 1)), b.y);
+            constexpr bool PLAIN = decltype(pn)::value;
+  #pragma unroll
+            for (int x4 = 0; x4 < TQJ / 4; ++x4) {
+              const float4 L4 = reinterpret_cast<const float4*>(sL)[x4];  // -lse
+              const float4 D4 = reinterpret_cast<const float4*>(sD)[x4];  // -D
+              const float2 nL[2] = {make_float2(L4.x, L4.y), make_float2(L4.z, L4.w)};
+              const float2 nD[2] = {make_float2(D4.x, D4.y), make_float2(D4.z, D4.w)};
+              float2 p[2], d[2];
+  #pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                const int c = 4 * x4 + 2 * h;
+                float2 v = make_float2(sr[c], sr[c + 1]);
+                if constexpr (CAP) v = cap_tanh<decltype(pl)::value>(P.cap, v);
+                float2 b = nL[h];
+                if constexpr (BIAS) {
+                  if constexpr (PLAIN) {
+                    b = add2(b, chain[(c >> 1) & 3]);
+                    chain[(c >> 1) & 3] = add2(chain[(c >> 1) & 3], step);
+                  } else {
+                    b.x = fmaf(-slope2, fabsf(d0 + (float)c), b.x);
+                    b.y = fmaf(-slope2, fabsf(d0 + (float)(c + 1)), b.y);
+                  }
                 }
+                const float2 t = fma2(v, in2, b);
+                p[h] = ((c >> 1) & 7) >= 8 - kBwdFma<CAP, BIAS> ? exp2_fma2_nan(t)
+                                                                : make_float2(ex2(t.x), ex2(t.y));
+                const float2 g = add2(make_float2(__uint_as_float(dr[c]), __uint_as_float(dr[c + 1])),
+                                      nD[h]);
+                if constexpr (CAP)  // (1 - tanh^2) g, the sign in the factor -p
+                  d[h] = mul2(mul2(g, mul2(p[h], make_float2(-1.f, -1.f))),
+                              fma2(v, v, make_float2(-1.f, -1.f)));
+                else
+                  d[h] = mul2_ftz(p[h], g);
               }
-              const float2 t = fma2(v, in2, b);
-              p[h] = ((c >> 1) & 7) >= 8 - kBwdFma<CAP, BIAS> ? exp2_fma2_nan(t)
-                                                              : make_float2(ex2(t.x), ex2(t.y));
-              const float2 g = add2(make_float2(__uint_as_float(dr[c]), __uint_as_float(dr[c + 1])),
-                                    nD[h]);
-              if constexpr (CAP)  // (1 - tanh^2) g, the sign in the factor -p
-                d[h] = mul2(mul2(g, mul2(p[h], make_float2(-1.f, -1.f))),
-                            fma2(v, v, make_float2(-1.f, -1.f)));
-              else
-                d[h] = mul2_ftz(p[h], g);
+              if constexpr (!PLAIN) {
+                const int4 B4 = reinterpret_cast<const int4*>(sB)[x4];
+                const int4 E4 = reinterpret_cast<const int4*>(sE)[x4];
+                const bool in0 = u >= B4.x && u < E4.x, in1 = u >= B4.y && u < E4.y;
+                const bool in2b = u >= B4.z && u < E4.z, in3 = u >= B4.w && u < E4.w;
+                // a row whose dout was cleaned has an infinite or NaN D, which p takes on
+                p[0].x = in0 ? fmaf(0.f, nD[0].x, p[0].x) : 0.f;
+                p[0].y = in1 ? fmaf(0.f, nD[0].y, p[0].y) : 0.f;
+                p[1].x = in2b ? fmaf(0.f, nD[1].x, p[1].x) : 0.f;
+                p[1].y = in3 ? fmaf(0.f, nD[1].y, p[1].y) : 0.f;
+                d[0].x = in0 ? d[0].x : 0.f;
+                d[0].y = in1 ? d[0].y : 0.f;
+                d[1].x = in2b ? d[1].x : 0.f;
+                d[1].y = in3 ? d[1].y : 0.f;
+              }
+              pp[2 * x4] = pack_bf16x2(p[0].x, p[0].y);
+              pp[2 * x4 + 1] = pack_bf16x2(p[1].x, p[1].y);
+              pd[2 * x4] = pack_bf16x2(d[0].x, d[0].y);
+              pd[2 * x4 + 1] = pack_bf16x2(d[1].x, d[1].y);
             }
-            if constexpr (!PLAIN) {
-              const int4 B4 = reinterpret_cast<const int4*>(sB)[x4];
-              const int4 E4 = reinterpret_cast<const int4*>(sE)[x4];
-              const bool in0 = u >= B4.x && u < E4.x, in1 = u >= B4.y && u < E4.y;
-              const bool in2b = u >= B4.z && u < E4.z, in3 = u >= B4.w && u < E4.w;
-              // a row whose dout was cleaned has an infinite or NaN D, which p takes on
-              p[0].x = in0 ? fmaf(0.f, nD[0].x, p[0].x) : 0.f;
-              p[0].y = in1 ? fmaf(0.f, nD[0].y, p[0].y) : 0.f;
-              p[1].x = in2b ? fmaf(0.f, nD[1].x, p[1].x) : 0.f;
-              p[1].y = in3 ? fmaf(0.f, nD[1].y, p[1].y) : 0.f;
-              d[0].x = in0 ? d[0].x : 0.f;
-              d[0].y = in1 ? d[0].y : 0.f;
-              d[1].x = in2b ? d[1].x : 0.f;
-              d[1].y = in3 ? d[1].y : 0.f;
-            }
-            pp[2 * x4] = pack_bf16x2(p[0].x, p[0].y);
-            pp[2 * x4 + 1] = pack_bf16x2(p[1].x, p[1].y);
-            pd[2 * x4] = pack_bf16x2(d[0].x, d[0].y);
-            pd[2 * x4 + 1] = pack_bf16x2(d[1].x, d[1].y);
-          }
           };
           by_flag(plain, [&](auto pn) {
             if (CAP && !poly) all(std::integral_constant<bool, false>{}, pn);
