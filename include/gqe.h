@@ -517,7 +517,8 @@ typedef struct {
  * gqe_attention_forward — out[s, b T + t] = sum of the weights times the values.
  *   lse   [S, B T] float32, device, 4-byte aligned, or NULL: written for the backward pass, the
  *         log2 of the row's sum of 2^(z log2 e) (-inf for a row without keys), as accurate as
- *         the bf16 weights need (2^-9 relative in the sum).
+ *         the bf16 weights need (2^-9 relative in the sum). It is a float32: beside
+ *         scores of some 10^4 and more the backward's weights lose a bit each time they double.
  * out must not overlap the inputs. B = 0 or T = 0 does nothing. One kernel launch; the result
  * is the same from run to run. A wait inside the kernel that gives up is reported by
  * gqe_check_op_status.
